@@ -346,6 +346,90 @@ tt_status tt_emb_backward_sgd_cached(tt_emb_plan_t plan, uint64_t kept_token, fl
                                      float* g3, float* hot_w, const float* grad_out, float lr,
                                      void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense operators on looked-up rows: layer norm, the gated feed-forward block
+ * and distillation from a teacher's top logits, forward and backward. They
+ * take bare device pointers and need no plan. All sums are held in fp32.
+ *
+ * Rows: a matrix [rows][cols] is given by its first element and its row
+ * stride in elements (ld >= cols), the columns contiguous; any width, stride
+ * and (element) alignment is served. Weights, statistics, lists and losses
+ * are contiguous. Zero rows are allowed: a forward then does nothing, a
+ * backward gives zero weight gradients. Outputs are fully overwritten and
+ * must not overlap inputs or each other.
+ *
+ * Workspaces are device buffers of the caller's, at least as large as the
+ * matching _workspace_bytes call says and 256-byte aligned; they hold nothing
+ * between calls, and calls that may run at the same time need one each. The
+ * _workspace_bytes calls are pure host computations and return 0 for sizes
+ * that are invalid or unsupported. The calls allocate nothing, wait for
+ * nothing and may be captured into a graph; every result is the same bits on
+ * every run. */
+typedef enum { TT_F32 = 0, TT_BF16 = 1, TT_F16 = 2 } tt_dtype;
+typedef enum { TT_ACT_SILU = 0, TT_ACT_GELU = 1, TT_ACT_RELU = 2 } tt_act;   /* gelu: the erf form */
+
+/* Layer norm: y = (x - mean) * rstd * weight + bias with the row's mean and
+ * rstd = 1/sqrt(var + eps), var the mean squared distance from the mean.
+ *   dtype   type of x, y, dy, dx
+ *   wdtype  type of weight, bias and their gradients: dtype or TT_F32
+ *   bias    may be NULL (and so may dbias)
+ *   mean, rstd  float[rows], what the backward needs; both NULL when serving
+ * Limits: dim <= 16384, rows < 2^31. */
+size_t tt_emb_norm_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim);
+tt_status tt_emb_norm_forward(int32_t dtype, int32_t wdtype, const void* x, int64_t ldx, const void* weight,
+                              const void* bias, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows,
+                              int64_t dim, float eps, void* stream);
+
+/* dx, dweight = sum over rows of dy * xhat, dbias = sum over rows of dy. */
+tt_status tt_emb_norm_backward(int32_t dtype, int32_t wdtype, const void* x, int64_t ldx, const void* weight,
+                               const float* mean, const float* rstd, const void* dy, int64_t lddy, void* dx,
+                               int64_t lddx, void* dweight, void* dbias, int64_t rows, int64_t dim, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Gated feed-forward block: out = act(x w_gate^T) * (x w_up^T), x [rows][dim],
+ * weights [hidden][dim], out [rows][hidden], all of type dtype.
+ *   gate, up  float[rows][hidden], the projections before the activation, as
+ *             the backward needs them; both NULL when serving
+ * TT_F32 products are formed from three bf16 parts of each operand to fp32
+ * accuracy; an infinity in an operand gives NaN. The backward's factors
+ * dout * up * act'(gate) and dout * act(gate) are rounded to dtype before
+ * their products, so with TT_F16 they must lie in its range.
+ * Limits: dim, hidden < 2^20, rows < 2^22, row stride of x < 2^22. */
+size_t tt_emb_gate_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden);
+tt_status tt_emb_gate_forward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate, const void* w_up,
+                              void* out, int64_t ldout, float* gate, float* up, int64_t rows, int64_t dim,
+                              int64_t hidden, int32_t act, void* workspace, size_t workspace_bytes, void* stream);
+tt_status tt_emb_gate_backward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate, const void* w_up,
+                               const float* gate, const float* up, const void* dout, int64_t lddout, void* dx,
+                               int64_t lddx, void* dw_gate, void* dw_up, int64_t rows, int64_t dim, int64_t hidden,
+                               int32_t act, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits. Row r's list is ids[r][top]
+ * (int64) and top_logits[r][top] (float): p = softmax(top_logits / T) over the
+ * list, q = softmax(logits / T) over all classes, T = temperature;
+ *   loss[r] = T^2 * sum_k p_k (log p_k - log q_{ids_k})
+ *   dlogits[r] = row_weight[r] * dloss[r]/dlogits
+ * An entry whose id is outside [0, classes) or whose logit is -inf is absent;
+ * a row without entries has loss 0 and gradient 0. A class listed twice gets
+ * the sum of its entries.
+ *   stats       float[rows][2], what a later backward needs; NULL when serving
+ *   row_weight  float[rows], the gradient of the objective in each row's loss
+ * tt_emb_distill_train is the forward and the backward in one call.
+ * Limits: 1e-18 <= temperature <= 1e18 (else TT_ERR_INVALID_ARG), classes <= 2^30, top <= 1024, rows * ceil(classes / 16384) < 2^31. */
+size_t tt_emb_distill_workspace_bytes(int32_t dtype, int64_t rows, int64_t classes);
+tt_status tt_emb_distill_forward(int32_t dtype, const void* logits, int64_t ld, const int64_t* ids,
+                                 const float* top_logits, int64_t top, float* loss, float* stats, int64_t rows,
+                                 int64_t classes, float temperature, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+tt_status tt_emb_distill_backward(int32_t dtype, const void* logits, int64_t ld, const int64_t* ids,
+                                  const float* top_logits, int64_t top, const float* stats, const float* row_weight,
+                                  void* dlogits, int64_t ldd, int64_t rows, int64_t classes, float temperature,
+                                  void* stream);
+tt_status tt_emb_distill_train(int32_t dtype, const void* logits, int64_t ld, const int64_t* ids,
+                               const float* top_logits, int64_t top, const float* row_weight, float* loss,
+                               void* dlogits, int64_t ldd, int64_t rows, int64_t classes, float temperature,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* tt_emb_status_string(tt_status s);
 

@@ -26,11 +26,16 @@ __all__ = [
     "tt_emb_kernel_times", "tt_emb_cache_bytes", "tt_emb_cache_build", "tt_emb_plan_cached",
     "tt_emb_forward_cached", "tt_emb_backward_cached", "tt_emb_backward_sgd_cached", "HotCache",
     "TT_PATH_MATRIX_CORE", "TT_PATH_GENERIC", "TT_ERR_STALE", "TT_ERR_SCRATCH", "TT_ERR_CACHE", "Plan",
+    "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
+    "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
+    "tt_emb_distill_backward", "tt_emb_distill_train",
     "EXPORTS",
 ]
 
 TT_OK = 0
 TT_ERR_INVALID_ARG = -1
+TT_ERR_UNSUPPORTED = -2
+TT_ERR_WORKSPACE = -3
 TT_ERR_DEVICE_FLAG = -5
 TT_ERR_STALE = -6
 TT_ERR_SCRATCH = -7
@@ -48,6 +53,9 @@ EXPORTS = (
     "tt_emb_query_paths", "tt_emb_forward_scratch", "tt_emb_scratch_capacity", "tt_emb_set_timing",
     "tt_emb_kernel_times", "tt_emb_cache_bytes", "tt_emb_cache_build", "tt_emb_plan_cached",
     "tt_emb_forward_cached", "tt_emb_backward_cached", "tt_emb_backward_sgd_cached", "tt_emb_status_string",
+    "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
+    "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
+    "tt_emb_distill_backward", "tt_emb_distill_train",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -140,11 +148,27 @@ def load_library() -> ctypes.CDLL:
         lib.tt_emb_backward_sgd_cached.argtypes = [P, ctypes.c_uint64, P, P, P, P, P, ctypes.c_float, P]
         lib.tt_emb_status_string.argtypes = [ctypes.c_int]
         lib.tt_emb_status_string.restype = ctypes.c_char_p
+        sz, f32 = ctypes.c_size_t, ctypes.c_float
+        for op in ("norm", "gate", "distill"):
+            getattr(lib, f"tt_emb_{op}_workspace_bytes").restype = sz
+        lib.tt_emb_norm_workspace_bytes.argtypes = [i32, i64, i64]
+        lib.tt_emb_gate_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        lib.tt_emb_distill_workspace_bytes.argtypes = [i32, i64, i64]
+        lib.tt_emb_norm_forward.argtypes = [i32, i32, P, i64, P, P, P, i64, P, P, i64, i64, f32, P]
+        lib.tt_emb_norm_backward.argtypes = [i32, i32, P, i64, P, P, P, P, i64, P, i64, P, P, i64, i64, P, sz, P]
+        lib.tt_emb_gate_forward.argtypes = [i32, P, i64, P, P, P, i64, P, P, i64, i64, i64, i32, P, sz, P]
+        lib.tt_emb_gate_backward.argtypes = [i32, P, i64, P, P, P, P, P, i64, P, i64, P, P, i64, i64, i64, i32, P,
+                                             sz, P]
+        lib.tt_emb_distill_forward.argtypes = [i32, P, i64, P, P, i64, P, P, i64, i64, f32, P, sz, P]
+        lib.tt_emb_distill_backward.argtypes = [i32, P, i64, P, P, i64, P, P, P, i64, i64, i64, f32, P]
+        lib.tt_emb_distill_train.argtypes = [i32, P, i64, P, P, i64, P, P, P, i64, i64, i64, f32, P, sz, P]
         for name in ("tt_emb_plan", "tt_emb_forward", "tt_emb_forward_train", "tt_emb_backward",
                      "tt_emb_backward_kept", "tt_emb_sgd", "tt_emb_get_error", "tt_emb_plan_get_view",
                      "tt_emb_plan_counts", "tt_emb_plan_destroy", "tt_emb_query_paths",
                      "tt_emb_cache_build", "tt_emb_plan_cached", "tt_emb_forward_cached",
-                     "tt_emb_backward_cached", "tt_emb_backward_sgd_cached"):
+                     "tt_emb_backward_cached", "tt_emb_backward_sgd_cached",
+                     "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_forward", "tt_emb_gate_backward",
+                     "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -479,3 +503,200 @@ def plan_table(plan: Plan, name: str, n: int):
     if off < 0 or off + 4 * n > plan.workspace.numel():
         raise ValueError(f"{name}[{n}] is outside the workspace")
     return plan.workspace[off:off + 4 * n].view(dtype=__import__("torch").int32)
+
+
+# ---------------------------------------------------------------------------
+# Dense operators: layer norm, the gated feed-forward block, distillation.
+
+_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1, "torch.float16": 2}
+_ACTS = {"silu": 0, "gelu": 1, "relu": 2}
+
+
+def _dtype_code(dtype, what: str) -> int:
+    code = _DTYPES.get(str(dtype))
+    if code is None:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _name(dtype) -> str:
+    return str(dtype).replace("torch.", "")
+
+
+def _matrix(t, dtype, what: str, rows: Optional[int] = None, cols: Optional[int] = None):
+    """(data_ptr, row stride) of a device matrix whose columns are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {_name(dtype)}, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        want = f"[{'rows' if rows is None else rows}, {'cols' if cols is None else cols}]"
+        raise ValueError(f"{what} must be {want}, got {list(t.shape)}")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous columns")
+    ld = int(t.stride(0)) if r > 1 else c
+    if ld < c:
+        raise ValueError(f"{what}'s rows overlap (row stride {ld}, {c} columns)")
+    return t.data_ptr(), ld
+
+
+def _pair(a, b, what: str):
+    """Whether two optional tensors are given; both or neither."""
+    if (a is None) != (b is None):
+        raise ValueError(f"{what}: give both or neither")
+    return a is not None
+
+
+def _workspace(workspace, need: int, what: str, device, stream):
+    """(tensor, data_ptr, bytes) of the caller's workspace, or of one allocated
+    here with torch on the stream that uses it."""
+    if need == 0:
+        raise TTEmbError(TT_ERR_UNSUPPORTED, what)
+    if workspace is None:
+        import torch
+        s = stream
+        if s is None:
+            s = torch.cuda.current_stream(device)
+        elif isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, device=device)
+        with torch.cuda.stream(s):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, _dev_ptr(workspace, "uint8", "workspace"), int(workspace.numel())
+
+
+def tt_emb_norm_workspace_bytes(dtype, rows: int, dim: int) -> int:
+    return int(load_library().tt_emb_norm_workspace_bytes(_dtype_code(dtype, "dtype"), rows, dim))
+
+
+def tt_emb_norm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+    """Layer norm of the rows of x [rows, dim] into y; mean and rstd
+    (float32[rows]) are kept for tt_emb_norm_backward when given."""
+    code, wcode = _dtype_code(x.dtype, "x"), _dtype_code(weight.dtype, "weight")
+    px, ldx = _matrix(x, x.dtype, "x")
+    rows, dim = x.shape
+    py, ldy = _matrix(y, x.dtype, "y", rows, dim)
+    _pair(mean, rstd, "mean and rstd")
+    wname = _name(weight.dtype)
+    _check(load_library().tt_emb_norm_forward(
+        code, wcode, px, ldx, _dev_ptr(weight, wname, "weight", dim), _dev_ptr(bias, wname, "bias", dim), py, ldy,
+        _dev_ptr(mean, "float32", "mean", rows), _dev_ptr(rstd, "float32", "rstd", rows), rows, dim, float(eps),
+        _stream(stream)), "tt_emb_norm_forward")
+
+
+def tt_emb_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias=None, workspace=None, stream=None):
+    """Gradients of tt_emb_norm_forward from the mean and rstd it kept."""
+    code, wcode = _dtype_code(x.dtype, "x"), _dtype_code(weight.dtype, "weight")
+    px, ldx = _matrix(x, x.dtype, "x")
+    rows, dim = x.shape
+    pdy, lddy = _matrix(dy, x.dtype, "dy", rows, dim)
+    pdx, lddx = _matrix(dx, x.dtype, "dx", rows, dim)
+    wname = _name(weight.dtype)
+    ws, pws, nws = _workspace(workspace, tt_emb_norm_workspace_bytes(x.dtype, rows, dim), "tt_emb_norm_backward",
+                              x.device, stream)
+    _check(load_library().tt_emb_norm_backward(
+        code, wcode, px, ldx, _dev_ptr(weight, wname, "weight", dim), _dev_ptr(mean, "float32", "mean", rows),
+        _dev_ptr(rstd, "float32", "rstd", rows), pdy, lddy, pdx, lddx, _dev_ptr(dweight, wname, "dweight", dim),
+        _dev_ptr(dbias, wname, "dbias", dim), rows, dim, pws, nws, _stream(stream)), "tt_emb_norm_backward")
+
+
+def tt_emb_gate_workspace_bytes(dtype, rows: int, dim: int, hidden: int) -> int:
+    return int(load_library().tt_emb_gate_workspace_bytes(_dtype_code(dtype, "dtype"), rows, dim, hidden))
+
+
+def _gate_sizes(x, w_gate, w_up, act):
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
+    code = _dtype_code(x.dtype, "x")
+    px, ldx = _matrix(x, x.dtype, "x")
+    rows, dim = x.shape
+    pg, ldg = _matrix(w_gate, x.dtype, "w_gate", None, dim)
+    hidden = int(w_gate.shape[0])
+    pu, ldu = _matrix(w_up, x.dtype, "w_up", hidden, dim)
+    if ldg != dim or ldu != dim:
+        raise ValueError("w_gate and w_up must be contiguous")
+    return code, px, ldx, pg, pu, int(rows), int(dim), hidden
+
+
+def tt_emb_gate_forward(x, w_gate, w_up, out, gate=None, up=None, act: str = "silu", workspace=None, stream=None):
+    """out = act(x w_gate^T) * (x w_up^T); gate and up (float32 [rows, hidden])
+    keep both projections for tt_emb_gate_backward when given."""
+    code, px, ldx, pg, pu, rows, dim, hidden = _gate_sizes(x, w_gate, w_up, act)
+    po, ldo = _matrix(out, x.dtype, "out", rows, hidden)
+    _pair(gate, up, "gate and up")
+    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes(x.dtype, rows, dim, hidden),
+                              "tt_emb_gate_forward", x.device, stream)
+    _check(load_library().tt_emb_gate_forward(
+        code, px, ldx, pg, pu, po, ldo, _dev_ptr(gate, "float32", "gate", rows * hidden),
+        _dev_ptr(up, "float32", "up", rows * hidden), rows, dim, hidden, _ACTS[act], pws, nws, _stream(stream)),
+        "tt_emb_gate_forward")
+
+
+def tt_emb_gate_backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, act: str = "silu", workspace=None,
+                         stream=None):
+    """Gradients of tt_emb_gate_forward from the projections it kept."""
+    code, px, ldx, pg, pu, rows, dim, hidden = _gate_sizes(x, w_gate, w_up, act)
+    pd, ldd = _matrix(dout, x.dtype, "dout", rows, hidden)
+    pdx, lddx = _matrix(dx, x.dtype, "dx", rows, dim)
+    name = _name(x.dtype)
+    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes(x.dtype, rows, dim, hidden),
+                              "tt_emb_gate_backward", x.device, stream)
+    _check(load_library().tt_emb_gate_backward(
+        code, px, ldx, pg, pu, _dev_ptr(gate, "float32", "gate", rows * hidden),
+        _dev_ptr(up, "float32", "up", rows * hidden), pd, ldd, pdx, lddx,
+        _dev_ptr(dw_gate, name, "dw_gate", hidden * dim), _dev_ptr(dw_up, name, "dw_up", hidden * dim), rows, dim,
+        hidden, _ACTS[act], pws, nws, _stream(stream)), "tt_emb_gate_backward")
+
+
+def tt_emb_distill_workspace_bytes(dtype, rows: int, classes: int) -> int:
+    return int(load_library().tt_emb_distill_workspace_bytes(_dtype_code(dtype, "dtype"), rows, classes))
+
+
+def _distill_sizes(logits, ids, top_logits):
+    code = _dtype_code(logits.dtype, "logits")
+    pz, ld = _matrix(logits, logits.dtype, "logits")
+    rows, classes = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != rows or ids.shape != top_logits.shape:
+        raise ValueError(f"ids and top_logits must be [{rows}, top], got {list(ids.shape)} and "
+                         f"{list(top_logits.shape)}")
+    top = int(ids.shape[1])
+    return (code, pz, ld, _dev_ptr(ids, "int64", "ids"), _dev_ptr(top_logits, "float32", "top_logits"), top,
+            int(rows), int(classes))
+
+
+def tt_emb_distill_forward(logits, ids, top_logits, loss, stats=None, temperature: float = 1.0, workspace=None,
+                           stream=None):
+    """Each row's loss against the teacher's list; stats (float32 [rows, 2])
+    is kept for tt_emb_distill_backward when given."""
+    code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
+    ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes(logits.dtype, rows, classes),
+                              "tt_emb_distill_forward", logits.device, stream)
+    _check(load_library().tt_emb_distill_forward(
+        code, pz, ld, pi, pt, top, _dev_ptr(loss, "float32", "loss", rows),
+        _dev_ptr(stats, "float32", "stats", rows * 2), rows, classes, float(temperature), pws, nws,
+        _stream(stream)), "tt_emb_distill_forward")
+
+
+def tt_emb_distill_backward(logits, ids, top_logits, stats, row_weight, dlogits, temperature: float = 1.0,
+                            stream=None):
+    """Gradient of sum(row_weight * loss) in the logits, from the stats the
+    forward kept."""
+    code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
+    pd, ldd = _matrix(dlogits, logits.dtype, "dlogits", rows, classes)
+    _check(load_library().tt_emb_distill_backward(
+        code, pz, ld, pi, pt, top, _dev_ptr(stats, "float32", "stats", rows * 2),
+        _dev_ptr(row_weight, "float32", "row_weight", rows), pd, ldd, rows, classes, float(temperature),
+        _stream(stream)), "tt_emb_distill_backward")
+
+
+def tt_emb_distill_train(logits, ids, top_logits, row_weight, loss, dlogits, temperature: float = 1.0,
+                         workspace=None, stream=None):
+    """tt_emb_distill_forward and tt_emb_distill_backward in one call."""
+    code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
+    pd, ldd = _matrix(dlogits, logits.dtype, "dlogits", rows, classes)
+    ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes(logits.dtype, rows, classes),
+                              "tt_emb_distill_train", logits.device, stream)
+    _check(load_library().tt_emb_distill_train(
+        code, pz, ld, pi, pt, top, _dev_ptr(row_weight, "float32", "row_weight", rows),
+        _dev_ptr(loss, "float32", "loss", rows), pd, ldd, rows, classes, float(temperature), pws, nws,
+        _stream(stream)), "tt_emb_distill_train")
