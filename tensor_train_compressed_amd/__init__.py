@@ -237,7 +237,8 @@ def core_extents(tables_c) -> tuple:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without making a Stream object (2.8 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -88,11 +88,10 @@ template <int P, class E>
 __device__ __forceinline__ void put_planes(E* __restrict__ dst, int64_t plane, const float (&f)[8]) {
     if constexpr (P == 1) {
         Raw8<E> o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = (E)f[e];
+        o.set(f);
         *reinterpret_cast<Raw8<E>*>(dst) = o;
     } else {
-        Raw8<bf16> o[3];
+        float o[3][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float x = f[e];
@@ -102,12 +101,16 @@ __device__ __forceinline__ void put_planes(E* __restrict__ dst, int64_t plane, c
                 x0 = (bf16)__uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
             const float r = fin ? x - (float)x0 : 0.f;
             const bf16 x1 = (bf16)r;
-            o[0].v[e] = x0;
-            o[1].v[e] = x1;
-            o[2].v[e] = (bf16)(r - (float)x1);
+            o[0][e] = (float)x0;
+            o[1][e] = (float)x1;
+            o[2][e] = r - (float)x1;
         }
 #pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<Raw8<bf16>*>(dst + p * plane) = o[p];
+        for (int p = 0; p < 3; ++p) {
+            Raw8<bf16> q;
+            q.set(o[p]);
+            *reinterpret_cast<Raw8<bf16>*>(dst + p * plane) = q;
+        }
     }
 }
 
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(256) void k_gate_pack(const T* __restrict__ src, in
     const Raw8<T> v = load8n(src + r * ld + c, cols - c, (T)0.f);
     float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = (float)v.v[e];
+    for (int e = 0; e < 8; ++e) f[e] = v.at(e);
     put_planes<Mat<T>::P>(dst + r * ldd + c, plane, f);
 }
 
@@ -146,7 +149,7 @@ __global__ __launch_bounds__(256) void k_gate_turn(const T* __restrict__ src, in
         const int64_t r = r0 + a + i;
         const Raw8<T> v = load8n(src + r * ld + c0 + b, r < rows ? cols - c0 - b : 0, (T)0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t.v[a + i][b + e] = (float)v.v[e];
+        for (int e = 0; e < 8; ++e) t.v[a + i][b + e] = v.at(e);
     }
     __syncthreads();
 #pragma unroll
@@ -182,9 +185,9 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float av, da;
-            act_grad<ACT>(g.v[e], av, da);
-            const float o = (float)d.v[e];
-            dg[e] = e < n ? o * u.v[e] * da : 0.f;
+            act_grad<ACT>(g.at(e), av, da);
+            const float o = d.at(e);
+            dg[e] = e < n ? o * u.at(e) * da : 0.f;
             du[e] = e < n ? o * av : 0.f;
             tg.v[a + i][b + e] = dg[e];
             tu.v[a + i][b + e] = du[e];
@@ -359,17 +362,16 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm(const Product q) {
         for (int v = 0; v < GROUP; v += 8) {
             const int n = q.N - nb - v;
             if (n <= 0) continue;
-            Raw8<T> o;
-            Raw8<float> g, u;
+            float o[8], g[8], u[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int j = (v + e) / 4, r = e & 3;
                 if constexpr (EPI == EPI_FWD) {
-                    g.v[e] = acc[i][j][r];
-                    u.v[e] = acc[i][j + FH][r];
-                    o.v[e] = (T)(act_of<ACT>(g.v[e]) * u.v[e]);
+                    g[e] = acc[i][j][r];
+                    u[e] = acc[i][j + FH][r];
+                    o[e] = act_of<ACT>(g[e]) * u[e];
                 } else {
-                    o.v[e] = (T)acc[i][j][r];
+                    o[e] = acc[i][j][r];
                 }
             }
             store8n(po + v, o, n);

@@ -85,25 +85,33 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_fwd(
         const Raw8<WT> rb = bias ? load8n(bias + c, n, (WT)0.f) : Raw8<WT>{};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            w[v * 8 + e] = (float)rw.v[e];
-            b[v * 8 + e] = bias ? (float)rb.v[e] : 0.f;
+            w[v * 8 + e] = rw.at(e);
+            b[v * 8 + e] = bias ? rb.at(e) : 0.f;
         }
     }
-    // rows of one wave or less need no barrier, so its groups may end apart
-    for (int64_t r = (int64_t)blockIdx.x * GPB + threadIdx.x / TPR; r < rows; r += (int64_t)gridDim.x * GPB) {
-        const T* px = x + r * ldx;
-        float f[E];
-        float s = 0.f, q = 0.f;
+    Raw8<T> rx[NV];
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + t) * 8;
-            const Raw8<T> rx = load8n(px + c, dim - c, (T)0.f);
+            rx[v] = load8n(x + r * ldx + c, dim - c, (T)0.f);
+        }
+    };
+    // rows of one wave or less need no barrier, so its groups may end apart
+    const int64_t step = (int64_t)gridDim.x * GPB;
+    int64_t r = (int64_t)blockIdx.x * GPB + threadIdx.x / TPR;
+    if (r < rows) fetch(r);
+    for (; r < rows; r += step) {
+        float f[E];
+        float s = 0.f, q = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                f[v * 8 + e] = (float)rx.v[e];
+                f[v * 8 + e] = rx[v].at(e);
                 s += f[v * 8 + e];
             }
-        }
+        if (r + step < rows) fetch(r + step);   // under way while this row is reduced
         row_sum2<TPR>(s, q, sm, slot);
         const float mean = s * inv_n;
         float var = 0.f;
@@ -124,9 +132,9 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_fwd(
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + t) * 8;
-            Raw8<T> o;
+            float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o.v[e] = (T)(f[v * 8 + e] * rstd * w[v * 8 + e] + b[v * 8 + e]);
+            for (int e = 0; e < 8; ++e) o[e] = f[v * 8 + e] * rstd * w[v * 8 + e] + b[v * 8 + e];
             store8n(py + c, o, dim - c);
         }
         if (t == 0 && mean_out) {
@@ -154,42 +162,54 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_bwd(
         const Raw8<WT> rw = load8n(weight + c, dim - c, (WT)0.f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            w[v * 8 + e] = (float)rw.v[e];
+            w[v * 8 + e] = rw.at(e);
             dw[v * 8 + e] = db[v * 8 + e] = 0.f;
         }
     }
-    for (int64_t r = (int64_t)blockIdx.x * GPB + threadIdx.x / TPR; r < rows; r += (int64_t)gridDim.x * GPB) {
-        const float mean = mean_in[r], rstd = rstd_in[r];
-        float h[E], g[E];   // xhat, dy
-        float s = 0.f, q = 0.f;
+    Raw8<T> rx[NV], rg[NV];
+    float mean_n, rstd_n;
+    auto fetch = [&](int64_t r) {
+        mean_n = mean_in[r];
+        rstd_n = rstd_in[r];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + t) * 8, n = dim - c;
-            const Raw8<T> rx = load8n(x + r * ldx + c, n, (T)0.f);
-            const Raw8<T> rg = load8n(dy + r * lddy + c, n, (T)0.f);
+            rx[v] = load8n(x + r * ldx + c, n, (T)0.f);
+            rg[v] = load8n(dy + r * lddy + c, n, (T)0.f);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * GPB;
+    int64_t r = (int64_t)blockIdx.x * GPB + threadIdx.x / TPR;
+    if (r < rows) fetch(r);
+    for (; r < rows; r += step) {
+        const float mean = mean_n, rstd = rstd_n;
+        float h[E], g[E];   // xhat, dy
+        float s = 0.f, q = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int k = v * 8 + e;
-                g[k] = (float)rg.v[e];   // 0 past the row's end, and so is every product below
-                h[k] = ((float)rx.v[e] - mean) * rstd;
+                g[k] = rg[v].at(e);   // 0 past the row's end, and so is every product below
+                h[k] = (rx[v].at(e) - mean) * rstd;
                 const float a = g[k] * w[k];
                 s += a;
                 q += a * h[k];
                 dw[k] += g[k] * h[k];
                 db[k] += g[k];
             }
-        }
+        if (r + step < rows) fetch(r + step);   // under way while this row is reduced
         row_sum2<TPR>(s, q, sm, slot);
         s *= inv_n;
         q *= inv_n;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + t) * 8;
-            Raw8<T> o;
+            float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int k = v * 8 + e;
-                o.v[e] = (T)(rstd * (g[k] * w[k] - s - h[k] * q));
+                o[e] = rstd * (g[k] * w[k] - s - h[k] * q);
             }
             store8n(dx + r * lddx + c, o, dim - c);
         }
@@ -242,6 +262,7 @@ __global__ __launch_bounds__(1024) void k_norm_wgrad(const float* __restrict__ p
     const int c = blockIdx.x * 16 + lc, k = blockIdx.y;
     float a = 0.f;
     if (c < dim)
+#pragma unroll 8
         for (int p = s; p < parts; p += 64) a += part[((int64_t)p * 2 + k) * dim + c];
     sm[s][lc] = a;
     __syncthreads();
