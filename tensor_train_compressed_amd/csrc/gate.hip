@@ -4,12 +4,14 @@
 //   dg = dout u act'(g),  du = dout act(g)
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
 //
-// Every product is one matrix-core kernel over operands whose summed index is
-// contiguous: D[m][n] = sum_k A[m][k] B[n][k]. The forward has that form as it
-// stands and forms both projections in one launch, act(g) u in its epilogue.
-// The backward lays out what it needs in the workspace: one pass over g, u and
-// dout writes [dg | du] and its transpose, and x and the weights are
-// transposed.
+// Every product is D[m][n] = sum_k A(m, k) B(n, k) on the matrix cores. An
+// operand lies in memory by rows (k contiguous: x and the weights in the
+// forward, dg and du in dx) or by columns (m or n contiguous: the weights in
+// dx, everything in dW); its tile keeps that layout in LDS, and the fragments
+// of a tile by columns are read with the transposing LDS load, so that nothing
+// is transposed in memory. The forward forms both projections in one launch
+// and act(g) u in its epilogue; the backward's dg and du are formed once, by
+// one pass over g, u and dout, into the workspace.
 //
 // Types. bf16 and f16 operands go to the matrix cores as they are; dg and du
 // are rounded to them (half a step of 2^-8 or 2^-11, the size of the error that
@@ -44,33 +46,66 @@ struct Frag<f16> {
     }
 };
 
-// What a tensor of type T is on the matrix cores: E elements, P planes.
+// What a tensor of type T is on the matrix cores: elements E in P planes, taken
+// BK at a time.
 template <class T>
 struct Mat {
     typedef T E;
-    static constexpr int P = 1;
+    static constexpr int P = 1, BK = 64;
 };
 template <>
 struct Mat<float> {
     typedef bf16 E;
-    static constexpr int P = 3;
+    static constexpr int P = 3, BK = 32;
 };
 
+// The planes of eight values.
+template <int P>
+struct Planes {
+    Raw8<bf16> p[P];
+};
+__device__ __forceinline__ void cut_planes(const float (&f)[8], Raw8<bf16> (&out)[3]) {
+    float x0[8], x1[8], x2[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // values that 8 digits would round up to infinity start from the largest finite one
+        constexpr float kTop = 3.38953139e38f;   // 0xFF 2^120
+        const float x = f[e];
+        x0[e] = (float)(bf16)__builtin_amdgcn_fmed3f(x, -kTop, kTop);
+        const float r = x - x0[e];
+        x1[e] = (float)(bf16)r;
+        x2[e] = r - x1[e];
+    }
+    out[0].set(x0);
+    out[1].set(x1);
+    out[2].set(x2);
+}
+// The six plane products, the smallest first.
+__device__ constexpr int kPlaneA[6] = {2, 0, 1, 1, 0, 0}, kPlaneB[6] = {0, 2, 1, 0, 1, 0};
+
 constexpr int kActs = 3;
-template <int ACT>
-__device__ __forceinline__ float act_of(float g) {
-    if (ACT == TT_ACT_SILU) return g / (1.f + expf(-g));
-    if (ACT == TT_ACT_GELU) return 0.5f * g * erfcf(-0.70710678118654752f * g);
+
+// 1 / (1 + e^-g). For results rounded to 16 bits by the hardware's 2^x and 1/x,
+// each within a step or two of fp32; a third of the instructions.
+template <class T>
+__device__ __forceinline__ float sigmoid(float g) {
+    if (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+    return 1.f / (1.f + expf(-g));
+}
+template <class T>
+__device__ __forceinline__ float act_of(int act, float g) {
+    if (act == TT_ACT_SILU) return g * sigmoid<T>(g);
+    if (act == TT_ACT_GELU) return 0.5f * g * erfcf(-0.70710678118654752f * g);
     return g > 0.f ? g : g == g ? 0.f : g;   // NaN stays NaN
 }
 // The activation and its derivative.
-template <int ACT>
-__device__ __forceinline__ void act_grad(float g, float& a, float& da) {
-    if (ACT == TT_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-g));
+template <class T>
+__device__ __forceinline__ void act_grad(int act, float g, float& a, float& da) {
+    if (act == TT_ACT_SILU) {
+        const float s = sigmoid<T>(g);
         a = g * s;
         da = s * (1.f + g * (1.f - s));
-    } else if (ACT == TT_ACT_GELU) {
+    } else if (act == TT_ACT_GELU) {
         const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
         a = g * cdf;
         da = cdf + g * (0.39894228040143268f * expf(-0.5f * g * g));
@@ -81,234 +116,332 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& da) {
 }
 
 // ---------------------------------------------------------------------------
-// Laying out operands.
+// dg and du, into gu [2][Hp / panel][M][panel] (Hp: H up to a multiple of kPanel,
+// zeros past H; panel: Hp for plain rows, or kPanel).
 
-// The planes of eight values, written `plane` elements apart.
-template <int P, class E>
-__device__ __forceinline__ void put_planes(E* __restrict__ dst, int64_t plane, const float (&f)[8]) {
-    if constexpr (P == 1) {
-        Raw8<E> o;
-        o.set(f);
-        *reinterpret_cast<Raw8<E>*>(dst) = o;
-    } else {
-        float o[3][8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = f[e];
-            bf16 x0 = (bf16)x;
-            const bool fin = fabsf(x) <= 3.402823466e38f;
-            if (fin && !(fabsf((float)x0) <= 3.402823466e38f))   // rounded up to infinity: cut instead
-                x0 = (bf16)__uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-            const float r = fin ? x - (float)x0 : 0.f;
-            const bf16 x1 = (bf16)r;
-            o[0][e] = (float)x0;
-            o[1][e] = (float)x1;
-            o[2][e] = r - (float)x1;
-        }
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            Raw8<bf16> q;
-            q.set(o[p]);
-            *reinterpret_cast<Raw8<bf16>*>(dst + p * plane) = q;
-        }
-    }
-}
-
-// dst[p][r][c] for c < ldd: src's rows, zeros past `cols` (ldd a multiple of 64).
 template <class T>
-__global__ __launch_bounds__(256) void k_gate_pack(const T* __restrict__ src, int64_t ld, int64_t rows, int cols,
-                                                   typename Mat<T>::E* __restrict__ dst, int64_t ldd,
-                                                   int64_t plane) {
-    const int64_t per = ldd / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t r = i / per;
-    const int c = (int)(i % per) * 8;
-    if (r >= rows) return;
-    const Raw8<T> v = load8n(src + r * ld + c, cols - c, (T)0.f);
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = v.at(e);
-    put_planes<Mat<T>::P>(dst + r * ldd + c, plane, f);
-}
-
-// A 64 x 64 tile in LDS, written by rows and read by columns.
-struct Tile64 {
-    float v[64][65];
-};
-
-// dst[p][c][r] for r < rowsp (a multiple of 64): src's columns, zeros past `rows`.
-template <class T>
-__global__ __launch_bounds__(256) void k_gate_turn(const T* __restrict__ src, int64_t ld, int64_t rows, int cols,
-                                                   typename Mat<T>::E* __restrict__ dst, int64_t ldd,
-                                                   int64_t plane) {
-    __shared__ Tile64 t;
-    const int64_t r0 = (int64_t)blockIdx.x * 64;
-    const int c0 = blockIdx.y * 64;
-    const int a = threadIdx.x >> 3, b = (threadIdx.x & 7) * 8;
-#pragma unroll
-    for (int i = 0; i < 64; i += 32) {
-        const int64_t r = r0 + a + i;
-        const Raw8<T> v = load8n(src + r * ld + c0 + b, r < rows ? cols - c0 - b : 0, (T)0.f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t.v[a + i][b + e] = v.at(e);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 64; i += 32) {
-        if (c0 + a + i >= cols) continue;
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = t.v[b + e][a + i];
-        put_planes<Mat<T>::P>(dst + (int64_t)(c0 + a + i) * ldd + r0 + b, plane, f);
-    }
-}
-
-// dg and du of a 64 x 64 tile: into gu [M][2 Hp] (dg, then du) and turned into
-// gut [2 Hp][Mp]. Zeros in [H, Hp) and in gut past M.
-template <class T, int ACT>
 __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gate, const float* __restrict__ up,
                                                    const T* __restrict__ dout, int64_t ldo, int64_t M, int H, int Hp,
-                                                   int64_t Mp, typename Mat<T>::E* __restrict__ gu, int64_t gu_plane,
-                                                   typename Mat<T>::E* __restrict__ gut, int64_t gut_plane) {
-    constexpr int P = Mat<T>::P;
-    __shared__ Tile64 tg, tu;
-    const int64_t m0 = (int64_t)blockIdx.x * 64;
-    const int h0 = blockIdx.y * 64;
-    const int a = threadIdx.x >> 3, b = (threadIdx.x & 7) * 8;
+                                                   int panel, int act, T* __restrict__ gu) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = Hp / 8;
+    const int64_t m = i / per;
+    const int h = (int)(i - m * per) * 8, n = H - h;
+    if (m >= M) return;
+    const Raw8<float> g = load8n(gate + m * H + h, n, 0.f), u = load8n(up + m * H + h, n, 0.f);
+    const Raw8<T> d = load8n(dout + m * ldo + h, n, (T)0.f);
+    float dg[8], du[8];
 #pragma unroll
-    for (int i = 0; i < 64; i += 32) {
-        const int64_t m = m0 + a + i;
-        const int n = m < M ? H - h0 - b : 0;
-        const Raw8<float> g = load8n(gate + m * H + h0 + b, n, 0.f);
-        const Raw8<float> u = load8n(up + m * H + h0 + b, n, 0.f);
-        const Raw8<T> d = load8n(dout + m * ldo + h0 + b, n, (T)0.f);
-        float dg[8], du[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float av, da;
-            act_grad<ACT>(g.at(e), av, da);
-            const float o = d.at(e);
-            dg[e] = e < n ? o * u.at(e) * da : 0.f;
-            du[e] = e < n ? o * av : 0.f;
-            tg.v[a + i][b + e] = dg[e];
-            tu.v[a + i][b + e] = du[e];
-        }
-        if (m < M) {
-            put_planes<P>(gu + m * 2 * Hp + h0 + b, gu_plane, dg);
-            put_planes<P>(gu + m * 2 * Hp + Hp + h0 + b, gu_plane, du);
-        }
+    for (int e = 0; e < 8; ++e) {
+        float a, da;
+        act_grad<T>(act, g.at(e), a, da);
+        const float o = d.at(e);
+        dg[e] = e < n ? o * u.at(e) * da : 0.f;
+        du[e] = e < n ? o * a : 0.f;
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 64; i += 32) {
-        float fg[8], fu[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            fg[e] = tg.v[b + e][a + i];
-            fu[e] = tu.v[b + e][a + i];
-        }
-        put_planes<P>(gut + (int64_t)(h0 + a + i) * Mp + m0 + b, gut_plane, fg);
-        put_planes<P>(gut + (int64_t)(Hp + h0 + a + i) * Mp + m0 + b, gut_plane, fu);
+    T* p = gu + (h / panel * M + m) * panel + h % panel;
+    store8n(p, dg, 8);
+    store8n(p + M * Hp, du, 8);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles in LDS.
+//
+// By rows: ROWS rows of BK elements; a row's 16-byte pieces are stored in the
+// order piece ^ key(row), so that the rows that lanes read together lie in
+// different banks.
+//
+// By columns: BK rows (the summed index k) of ROWS elements; a row's 32-byte
+// blocks are stored in the order block ^ (k & 3 | k >> 3 & 1): the transposing
+// load of 16 lanes takes 32 bytes of four rows k, and four such groups are 8
+// rows apart.
+
+// Elements of a line that lie together in an operand cut into panels: [panel]
+// [line][kPanel]. A step's tile by rows is then one piece of memory.
+constexpr int kPanel = 32;
+
+template <int BK>
+__device__ __forceinline__ int row_slot(int row, int piece) {
+    return piece ^ (BK == 64 ? row & 7 : (row >> 1) & 3);
+}
+__device__ __forceinline__ int col_key(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+
+// Byte offset of 16-byte piece `piece` of line `line` (a row, or a k).
+template <bool COLS, int BK, int ROWS>
+__device__ __forceinline__ int lds_piece(int line, int piece) {
+    if (COLS) return line * (ROWS * 2) + ((piece >> 1) ^ col_key(line)) * 32 + (piece & 1) * 16;
+    return line * (BK * 2) + row_slot<BK>(line, piece) * 16;
+}
+
+// The fragment of 16 rows (or columns) x 32 k, k in [32 h, 32 h + 32): lane l
+// holds 8 consecutive k, from 8 (l / 16), of its row. By rows the lane's row
+// is `row`; by columns the fragment's columns are row0 + 0..15.
+template <class V, bool COLS, int BK, int ROWS>
+__device__ __forceinline__ V fragment(const char* lds, int row, int row0, int h) {
+    const int lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
+    if constexpr (!COLS) {
+        return *reinterpret_cast<const V*>(lds + lds_piece<false, BK, ROWS>(row, h * 4 + lk));
+    } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const int k = h * 32 + lk * 8 + (li >> 2);   // this lane's addresses: 4 columns of rows k and k + 4
+        const char* p = lds + k * (ROWS * 2) + ((row0 >> 4) ^ col_key(k)) * 32 + (li & 3) * 8;
+        auto at = [](const char* q) {
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)q);
+        };
+        const s16x4 a = at(p), b = at(p + 4 * ROWS * 2);
+        return __builtin_bit_cast(V, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 }
 
 // ---------------------------------------------------------------------------
-// The product. A workgroup of four waves forms a 128 x 128 tile of D, 64 of
-// the summed index at a time: both operands' tiles go from memory straight to
-// LDS, the next ones while the matrix cores work on these. A tile's row is 128
-// bytes, eight 16-byte pieces that are stored in the order piece ^ key(row),
-// so that the 16 rows a wave reads at once lie in different banks.
+// The products.
 
-constexpr int kBK = 64;
-
-struct Operand {
-    const void* p;     // rows of `ld` elements, the summed index contiguous
-    int64_t ld, plane; // elements from row to row, from plane to plane
-    int64_t rows;      // rows past the last one are read as the last one (their results are dropped)
-};
+enum Kind { FWD, DX, DW };
+// FWD: A = x and B = both weights by rows; DX: A = [dg | du] by rows, B = the
+// weights by columns, one after the other; DW: A = dg or du and B = x by columns.
 
 struct Product {
-    Operand a, b, b2;   // b2: the second projection's weight (forward)
+    const void *a, *b, *b2;      // b2: the second weight (FWD, DX)
+    int64_t lda, ldb;            // elements from line to line
+    int64_t pa, pb;              // elements from panel to panel (kPanel elements of each line); kPanel: plain rows
+    int64_t bytes_a, bytes_b;    // of a, and of b and b2 each
     int64_t M;
-    int N, kp;          // kp: summed length, a multiple of kBK (both operands hold zeros past the real one)
-    void *out, *out2;   // out2: of the second half of a's rows (weight gradients), blockIdx.z = 1
+    int N;
+    int64_t K;                   // summed length; of each of two parts in DX
+    int64_t a2;                  // elements from dg to du (DX, DW)
+    void *out, *out2;            // out2: of du (DW)
     int64_t ldo;
-    float *gate, *up;   // forward, or null: g and u, [M][N]
+    float *gate, *up;            // FWD: g and u [M][N], or null
+    int act;
+    float* part;                 // partial sums, when the summed length is split: [split][FWD: 2, DW: 2][M][N]
+    int steps, split_steps;      // BK-steps in all, and of a split
+    int mt, nt;                  // tiles
 };
 
-enum { EPI_FWD, EPI_OUT };
-
-// The planes of the six products of fp32 operands, the smallest products first.
-__device__ __forceinline__ int plane_a(int s) { return (0x001102 >> (4 * s)) & 3; }   // 2 0 1 1 0 0
-__device__ __forceinline__ int plane_b(int s) { return (0x010120 >> (4 * s)) & 3; }   // 0 2 1 0 1 0
-
-template <int ROWS, int GROUP>
-__device__ __forceinline__ int lds_key(int row) {
-    return (row & 3) | (((row / GROUP) & 1) << 2);
+// Tile of a workgroup: workgroups run on XCD blockIdx mod 8, so each XCD takes
+// a run of consecutive tiles, and a run goes down bands of 8 rows of tiles,
+// whose operands its L2 then holds.
+__device__ __forceinline__ void tile_of(const Product& q, int& tm, int& tn) {
+    const int all = q.mt * q.nt, per = all / kXcds, rest = all % kXcds;
+    const int x = blockIdx.x % kXcds;
+    const int t = x * per + min(x, rest) + blockIdx.x / kXcds;
+    const int band = t / (8 * q.nt), rows = min(8, q.mt - band * 8), in = t - band * 8 * q.nt;
+    tm = band * 8 + in % rows;
+    tn = in / rows;
 }
 
-// Loads a wave's part of a ROWS x kBK tile: offsets of its 16-byte pieces
-// (bytes from the tile's first row), one instruction for 8 rows.
-template <int ROWS, int GROUP, int WAVES>
-struct TileLoad {
-    static constexpr int N = ROWS / 8 / WAVES;
-    uint32_t off[N];
-    const char* base;
-    __device__ __forceinline__ void init(const Operand& o, int64_t row0) {
-        base = (const char*)o.p + row0 * o.ld * 2;
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+// A tile's loads straight to LDS, 16 bytes a lane and 1024 an instruction. The
+// buffer descriptor starts at the tile's first line of the step and ends with
+// the operand, past which the loads deliver zeros. What lies past the summed
+// length is given an offset outside the buffer, for zeros too. (Lines and pieces
+// past the last row or column of D may read what follows in the operand; their
+// results are dropped.)
+template <bool COLS, int BK, int ROWS, int WAVES>
+struct DmaLoad {
+    static constexpr int N = ROWS * BK * 2 / 1024 / WAVES;    // instructions of a wave
+    static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;   // of a line
+    static constexpr int LINES = 64 / PIECES;                 // of an instruction
+    uint32_t off[N];   // of this lane's piece from the instruction's first line
+    uint32_t line;     // bytes from line to line
+    int wave;
+    __device__ __forceinline__ int piece(int i) const {
+        const int lane = threadIdx.x & 63, l = (wave * N + i) * LINES + lane / PIECES, s = lane % PIECES;
+        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot<BK>(l, s);
+    }
+    __device__ __forceinline__ void init(int64_t ld, int64_t panel) {
+        line = (uint32_t)ld * 2;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = (wave * N + i) * 8 + (lane >> 3), c = (lane & 7) ^ lds_key<ROWS, GROUP>(r);
-            const int64_t last = o.rows - 1 - row0;
-            off[i] = (uint32_t)((r < last ? r : last) * o.ld * 2 + c * 16);
+            const int p = piece(i);
+            off[i] = (threadIdx.x & 63) / PIECES * line + p / (kPanel / 8) * (uint32_t)panel * 2 + p % (kPanel / 8) * 16;
         }
     }
-    // k: bytes along the row (and to the plane)
-    __device__ __forceinline__ void load(char* lds, int64_t k) const {
-        const int wave = threadIdx.x >> 6;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)(base + k + off[i]),
-                                             (__attribute__((address_space(3))) void*)(lds + (wave * N + i) * 1024),
-                                             16, 0, 0);
+    // Instruction i. base: the tile's first line at this step; bytes: from there
+    // to the operand's end; left: of the summed length
+    __device__ __forceinline__ void load(int i, char* lds, const char* base, int64_t bytes, int64_t left) const {
+#ifdef __HIP_DEVICE_COMPILE__   // the descriptor's type is the device compiler's
+        const int n = left < BK ? (int)left : BK;
+        const int64_t size = left <= 0 || bytes < 0 ? 0 : bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)size, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * N + i) * 1024), 16,
+            (COLS ? (wave * N + i) * LINES + (int)(threadIdx.x & 63) / PIECES : piece(i) * 8) < n ? off[i] : 0x80000000u,
+            (wave * N + i) * LINES * line, 0, 0);
+#endif
     }
 };
 
-__device__ __forceinline__ void loads_done_barrier() {
-    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's loads to LDS have landed
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+// The same tile through registers: any alignment, and fp32, cut into planes on
+// its way to LDS.
+template <class T, bool COLS, int BK, int ROWS, int THREADS>
+struct RegLoad {
+    static constexpr int P = Mat<T>::P, N = ROWS * BK / 8 / THREADS;
+    static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;
+    Raw8<T> r[N];
+    __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int64_t row0, int64_t rows, int64_t k0,
+                                         int64_t K) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = i * THREADS + threadIdx.x, line = id / PIECES, piece = id % PIECES;
+            const int64_t l = COLS ? k0 + line : row0 + line, e = (COLS ? row0 : k0) + piece * 8;
+            const int64_t n = l < (COLS ? K : rows) ? (COLS ? rows : K) - e : 0;
+            r[i] = load8n(p + l * ld + e, (int)(n < 8 ? n : 8), (T)0.f);
+        }
+    }
+    __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = i * THREADS + threadIdx.x, line = id / PIECES, piece = id % PIECES;
+            char* q = lds + lds_piece<COLS, BK, ROWS>(line, piece);
+            if constexpr (P == 1) {
+                *reinterpret_cast<Raw8<T>*>(q) = r[i];
+            } else {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = r[i].at(e);
+                Raw8<bf16> c[3];
+                cut_planes(f, c);
+#pragma unroll
+                for (int s = 0; s < 3; ++s) *reinterpret_cast<Raw8<bf16>*>(q + s * ROWS * BK * 2) = c[s];
+            }
+        }
+    }
+};
+
+// What a kernel's waves and tiles are: WM x WN waves, FM x FN fragments each.
+template <Kind KIND, int WM, int WN, int FM, int FN>
+struct Shape {
+    static constexpr int THREADS = WM * WN * 64, TM = WM * FM * 16, TN = WN * FN * 16;
+    static constexpr bool AC = KIND == DW, BC = KIND != FWD;
+    static constexpr int FH = KIND == FWD ? FN / 2 : FN;  // fragments of D's columns in a wave
+    static constexpr int NB = KIND == FWD ? TN / 2 : TN;  // columns of D of a workgroup
+    // (FWD: LDS rows [0, NB) of B are Wg's, [NB, TN) Wu's, and so are a wave's fragments)
+};
+
+// Results of a wave. acc[i][j][r] is D[m][n], m = i * 16 + lane % 16 and
+// n = j * 16 + lane / 16 * 4 + r; in FWD g for j < FH, and u FH fragments on.
+template <class T, Kind KIND, class S, int FM, int FN>
+__device__ __forceinline__ void put_out(const Product& q, const floatx4 (&acc)[FM][FN], int64_t m0, int n0) {
+    const int li = threadIdx.x & 15, lk = (threadIdx.x & 63) >> 4;
+    const int64_t MN = q.M * q.N;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        __builtin_amdgcn_sched_barrier(0);   // row by row: no registers for several at once
+        const int64_t m = m0 + i * 16 + li;
+        if (m >= q.M) continue;
+#pragma unroll
+        for (int j = 0; j < S::FH; ++j) {
+            const int n = n0 + j * 16 + lk * 4, left = q.N - n;
+            if (left <= 0) continue;
+            const float d[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            if constexpr (KIND == FWD) {
+                const floatx4 v = acc[i][j + S::FH];
+                const float u[4] = {v[0], v[1], v[2], v[3]};
+                float *pg = q.gate, *pu = q.up;
+                if (q.part) {
+                    pg = q.part + blockIdx.y * 2 * MN;
+                    pu = pg + MN;
+                } else {
+                    float o[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[r] = act_of<T>(q.act, d[r]) * u[r];
+                    store4n((T*)q.out + m * q.ldo + n, o, left);
+                }
+                if (pg) {
+                    store4n(pg + m * q.N + n, d, left);
+                    store4n(pu + m * q.N + n, u, left);
+                }
+            } else if (q.part) {
+                store4n(q.part + (blockIdx.y * gridDim.z + blockIdx.z) * MN + m * q.N + n, d, left);
+            } else {
+                store4n((T*)(blockIdx.z ? q.out2 : q.out) + m * q.ldo + n, d, left);
+            }
+        }
+    }
 }
 
-template <class T, int EPI, int ACT>
-__global__ __launch_bounds__(256, 2) void k_gate_mm(const Product q) {
-    typedef typename Mat<T>::E E;
-    typedef typename Frag<E>::V V;
-    constexpr int P = Mat<T>::P, SEGS = P == 1 ? 1 : 6;
-    constexpr int TM = 128, TN = 128, FM = 4, FN = 4, WAVES = 4;
-    constexpr int FH = EPI == EPI_FWD ? FN / 2 : FN;   // fragments of consecutive columns
-    constexpr int GROUP = 4 * FH;                      // consecutive columns a lane ends up with
-    constexpr int NB = EPI == EPI_FWD ? TN / 2 : TN;   // columns of D a workgroup forms
-    __shared__ __align__(16) char sa0[TM * 128], sb0[TN * 128], sa1[TM * 128], sb1[TN * 128];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
-    const int n0 = blockIdx.x * NB;
-    const int64_t m0 = (int64_t)blockIdx.y * TM;
-    Operand oa = q.a;
-    if (EPI == EPI_OUT) oa.p = (const char*)oa.p + blockIdx.z * oa.rows * oa.ld * 2;
+// Waits until at most LEFT of this wave's loads to LDS are under way, and its LDS
+// reads are done, then for the workgroup's other waves.
+template <int LEFT>
+__device__ __forceinline__ void landed_barrier() {
+    // (fences for the compiler only: a workgroup fence would wait for every load under way)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((LEFT & 15) | 0x0070 | (LEFT >> 4) << 14);   // vmcnt(LEFT) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
-    TileLoad<TM, 4, WAVES> la;
-    TileLoad<NB, GROUP, WAVES> lb, lb2;
-    la.init(oa, m0);
-    lb.init(q.b, n0);
-    if (EPI == EPI_FWD) lb2.init(q.b2, n0);
-    const int nk = q.kp / kBK, steps = nk * SEGS;
-    auto load = [&](char* sa, char* sb, int step) {
-        const int s = SEGS == 1 ? 0 : step / nk;
-        const int64_t k = (int64_t)(step - s * nk) * (kBK * 2);
-        la.load(sa, k + (SEGS == 1 ? 0 : plane_a(s) * oa.plane * 2));
-        lb.load(sb, k + (SEGS == 1 ? 0 : plane_b(s) * q.b.plane * 2));
-        if (EPI == EPI_FWD) lb2.load(sb + NB * 128, k + (SEGS == 1 ? 0 : plane_b(s) * q.b2.plane * 2));
+// acc[j] += b[j] a for a row of fragments, in place in the accumulation
+// registers. (With all 256 of them in use the compiler's own choice moves
+// accumulators to and fro, 100 moves a step.) The leading wait covers operands
+// that a vector instruction has just written.
+template <class T, class V, int FN>
+__device__ __forceinline__ void mma_row(floatx4 (&c)[FN], const V& a, const V (&b)[FN]) {
+    static_assert(FN == 4 || FN == 8, "fragments of a row");
+#define TT_MMA4(OP, J)                                                                                       \
+    asm volatile("s_nop 1\n\t" OP " %0, %4, %8, %0\n\t" OP " %1, %5, %8, %1\n\t" OP " %2, %6, %8, %2\n\t" OP \
+                 " %3, %7, %8, %3"                                                                           \
+                 : "+a"(c[J]), "+a"(c[J + 1]), "+a"(c[J + 2]), "+a"(c[J + 3])                                \
+                 : "v"(b[J]), "v"(b[J + 1]), "v"(b[J + 2]), "v"(b[J + 3]), "v"(a))
+#pragma unroll
+    for (int j = 0; j < FN; j += 4) {
+        if constexpr (std::is_same<T, bf16>::value) TT_MMA4("v_mfma_f32_16x16x32_bf16", j);
+        else TT_MMA4("v_mfma_f32_16x16x32_f16", j);
+    }
+#undef TT_MMA4
+}
+
+// Waits until the matrix instructions' results can be read: 32 cycles, tied to
+// the accumulators that are read next.
+template <int FN>
+__device__ __forceinline__ void mma_done(floatx4 (&c)[FN]) {
+#pragma unroll
+    for (int j = 0; j < FN; j += 4)
+        asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[j]), "+a"(c[j + 1]), "+a"(c[j + 2]), "+a"(c[j + 3]));
+}
+
+// 16-bit operands whose pieces are whole and aligned: tiles of 32 of the summed
+// length go from memory straight to LDS, through a ring of four. While the
+// matrix cores work on a step, whose fragments are in registers, the next
+// step's fragments are read and the loads of the one four steps on are issued,
+// both spread over the products: three steps are under way all the time, which
+// covers the latency of the caches past L2. One barrier a step.
+template <class T, Kind KIND, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(const Product q) {
+    typedef Shape<KIND, WM, WN, FM, FN> S;
+    typedef typename Frag<T>::V V;
+    constexpr int BK = 32, WAVES = WM * WN;
+    // separate objects, so that the compiler sees which loads a read depends on
+    __shared__ __align__(16) char sa0[S::TM * BK * 2], sb0[S::TN * BK * 2], sa1[S::TM * BK * 2], sb1[S::TN * BK * 2],
+        sa2[S::TM * BK * 2], sb2[S::TN * BK * 2], sa3[S::TM * BK * 2], sb3[S::TN * BK * 2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN, li = lane & 15;
+    int tm, tn;
+    tile_of(q, tm, tn);
+    const int64_t m0 = (int64_t)tm * S::TM;
+    const int n0 = tn * S::NB;
+    const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
+
+    DmaLoad<S::AC, BK, S::TM, WAVES> la;
+    DmaLoad<S::BC, BK, S::NB, WAVES> lb;
+    la.init(q.lda, q.pa);
+    lb.init(q.ldb, q.pb);
+    constexpr int LOADS = la.N + lb.N * (KIND == FWD ? 2 : 1);   // a wave's a step
+    static_assert(BK == kPanel && S::TM % kPanel == 0 && S::NB % kPanel == 0, "tiles are whole panels");
+    const int64_t ta = (S::AC ? m0 / kPanel * q.pa : m0 * q.lda) * 2 + (KIND == DW ? (int64_t)blockIdx.z * q.a2 * 2 : 0);
+    const int64_t tb = (S::BC ? n0 / kPanel * q.pb : n0 * q.ldb) * 2;
+    const int half = KIND == DX ? q.steps / 2 : q.steps;
+    // load x of a step; steps past the last one are zeros
+    auto load = [&](char* sa, char* sb, int step, int x) {
+        const bool second = KIND == DX && step >= half;
+        const int64_t k = (int64_t)(second ? step - half : step) * BK, left = step < s1 ? q.K - k : 0;
+        const int64_t oa = ta + (S::AC ? k * q.lda : k / kPanel * q.pa + (second ? q.a2 : 0)) * 2;
+        const int64_t ob = tb + (S::BC ? k * q.ldb : k / kPanel * q.pb) * 2;
+        if (x < la.N) la.load(x, sa, (const char*)q.a + oa, q.bytes_a - oa, left);
+        else if (x < la.N + lb.N) lb.load(x - la.N, sb, (const char*)(second ? q.b2 : q.b) + ob, q.bytes_b - ob, left);
+        else if (KIND == FWD) lb.load(x - la.N - lb.N, sb + S::NB * BK * 2, (const char*)q.b2 + ob, q.bytes_b - ob, left);
     };
 
     floatx4 acc[FM][FN];
@@ -317,69 +450,276 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm(const Product q) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-    const int li = lane & 15, lk = lane >> 4;
-    auto compute = [&](const char* sa, const char* sb) {
+    // fragment x of a step: B's first, which every row of products needs, then A's
+    V f0[FN + FM], f1[FN + FM];
+    auto read = [&](V (&f)[FN + FM], const char* sa, const char* sb, int x) {
+        if (x < FN) {
+            const int w = (wn * S::FH + x % S::FH) * 16;
+            f[x] = fragment<V, S::BC, BK, S::NB>(sb + x / S::FH * S::NB * BK * 2, w + li, w, 0);
+        } else {
+            const int r = wm * FM * 16 + (x - FN) * 16;
+            f[x] = fragment<V, S::AC, BK, S::TM>(sa, r + li, r, 0);
+        }
+    };
+    // Step s: products of its fragments f; fragments g of step s + 1 from (ta, tb), early enough
+    // that the last arrive before they are needed; loads of step s + 4 into (sa, sb), step s's own.
+    auto step = [&](int s, V (&f)[FN + FM], V (&g)[FN + FM], char* sa, char* sb, const char* ta, const char* tb) {
+        landed_barrier<2 * LOADS>();   // step s + 1 is there, s + 2 and s + 3 may be under way
+        constexpr int PER = (FN + FM + FM - 2) / (FM - 1);
 #pragma unroll
-        for (int h = 0; h < kBK / 32; ++h) {
-            V fa[FM], fb[FN];
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int r = wm * FM * 16 + i * 16 + li;
-                fa[i] = *reinterpret_cast<const V*>(sa + r * 128 + ((h * 4 + lk) ^ lds_key<TM, 4>(r)) * 16);
-            }
+            for (int x = i * PER; x < (i + 1) * PER && x < FN + FM; ++x) read(g, ta, tb, x);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int w = wn * FH * 16 + (li >> 2) * GROUP + (j % FH) * 4 + (li & 3);
-                const int r = (j / FH) * NB + w;
-                fb[j] = *reinterpret_cast<const V*>(sb + r * 128 + ((h * 4 + lk) ^ lds_key<NB, GROUP>(w)) * 16);
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = Frag<E>::mma(fb[j], fa[i], acc[i][j]);
+            for (int x = i * LOADS / FM; x < (i + 1) * LOADS / FM; ++x) load(sa, sb, s + 4, x);
+            mma_row<T>(acc[i], f[FN + i], reinterpret_cast<const V(&)[FN]>(f));
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    if (steps > 0) load(sa0, sb0, 0);
-    for (int s = 0; s < steps; s += 2) {
-        loads_done_barrier();
-        if (s + 1 < steps) load(sa1, sb1, s + 1);
-        compute(sa0, sb0);
-        if (s + 1 >= steps) break;
-        loads_done_barrier();
-        if (s + 2 < steps) load(sa0, sb0, s + 2);
-        compute(sa1, sb1);
+    if (s0 < s1) {
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x) load(sa0, sb0, s0, x);
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x) load(sa1, sb1, s0 + 1, x);
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x) load(sa2, sb2, s0 + 2, x);
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x) load(sa3, sb3, s0 + 3, x);
+        landed_barrier<3 * LOADS>();
+#pragma unroll
+        for (int x = 0; x < FN + FM; ++x) read(f0, sa0, sb0, x);
+        for (int s = s0; s < s1; s += 4) {   // up to three steps of zeros at the end
+            step(s, f0, f1, sa0, sb0, sa1, sb1);
+            step(s + 1, f1, f0, sa1, sb1, sa2, sb2);
+            step(s + 2, f0, f1, sa2, sb2, sa3, sb3);
+            step(s + 3, f1, f0, sa3, sb3, sa0, sb0);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0f70);   // no load to LDS outlives the workgroup
     }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) mma_done(acc[i]);
+    put_out<T, KIND, S>(q, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
+}
 
-    // acc[i][j][r] is D[m][n] with m = .. + i*16 + lane%16 and n consecutive over (j, r)
-    const int nb = n0 + wn * FH * 16 + lk * GROUP;
+// Operands of any type and alignment: tiles pass through registers, loaded
+// while the matrix cores work on the step before.
+template <class T, Kind KIND>
+__global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
+    constexpr int FM = 4, FN = 4, WM = 2, WN = 2;
+    typedef Shape<KIND, WM, WN, FM, FN> S;
+    typedef typename Mat<T>::E E;
+    typedef typename Frag<E>::V V;
+    constexpr int BK = Mat<T>::BK, P = Mat<T>::P;
+    constexpr int PA = S::TM * BK * 2, PB = S::NB * BK * 2, NB2 = KIND == FWD ? 2 : 1;   // bytes of a plane
+    __shared__ __align__(16) char sa[P * PA], sb[NB2 * P * PB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN, li = lane & 15;
+    int tm, tn;
+    tile_of(q, tm, tn);
+    const int64_t m0 = (int64_t)tm * S::TM;
+    const int n0 = tn * S::NB;
+    const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
+
+    RegLoad<T, S::AC, BK, S::TM, 256> la;
+    RegLoad<T, S::BC, BK, S::NB, 256> lb, lb2;
+    const T* pa = (const T*)q.a + (KIND == DW ? (int64_t)blockIdx.z * q.a2 : 0);
+    const int half = KIND == DX ? q.steps / 2 : q.steps;
+    auto load = [&](int step) {
+        const bool second = KIND == DX && step >= half;
+        const int64_t k = (int64_t)(second ? step - half : step) * BK;
+        la.load(pa + (second ? q.a2 : 0), q.lda, m0, q.M, k, q.K);
+        lb.load((const T*)(second ? q.b2 : q.b), q.ldb, n0, q.N, k, q.K);
+        if constexpr (KIND == FWD) lb2.load((const T*)q.b2, q.ldb, n0, q.N, k, q.K);
+    };
+
+    floatx4 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int64_t m = m0 + wm * FM * 16 + i * 16 + li;
-        if (m >= q.M) continue;
-        T* po = (T*)(blockIdx.z ? q.out2 : q.out) + m * q.ldo + nb;
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int v = 0; v < GROUP; v += 8) {
-            const int n = q.N - nb - v;
-            if (n <= 0) continue;
-            float o[8], g[8], u[8];
+        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    if (s0 < s1) load(s0);
+    for (int s = s0; s < s1; ++s) {
+        __syncthreads();
+        la.store(sa);
+        lb.store(sb);
+        if constexpr (KIND == FWD) lb2.store(sb + P * PB);
+        __syncthreads();
+        if (s + 1 < s1) load(s + 1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int j = (v + e) / 4, r = e & 3;
-                if constexpr (EPI == EPI_FWD) {
-                    g[e] = acc[i][j][r];
-                    u[e] = acc[i][j + FH][r];
-                    o[e] = act_of<ACT>(g[e]) * u[e];
+        for (int h = 0; h < BK / 32; ++h) {
+            V fa[P][FM];
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int r = wm * FM * 16 + i * 16;
+                    fa[p][i] = fragment<V, S::AC, BK, S::TM>(sa + p * PA, r + li, r, h);
+                }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                V fb[P];
+                const int w = (wn * S::FH + j % S::FH) * 16;
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    fb[p] = fragment<V, S::BC, BK, S::NB>(sb + (j / S::FH * P + p) * PB, w + li, w, h);
+                if constexpr (P == 1) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) acc[i][j] = Frag<E>::mma(fb[0], fa[0][i], acc[i][j]);
                 } else {
-                    o[e] = acc[i][j][r];
+#pragma unroll
+                    for (int t = 0; t < 6; ++t)
+#pragma unroll
+                        for (int i = 0; i < FM; ++i)
+                            acc[i][j] = Frag<E>::mma(fb[kPlaneB[t]], fa[kPlaneA[t]][i], acc[i][j]);
                 }
             }
-            store8n(po + v, o, n);
-            if constexpr (EPI == EPI_FWD)
-                if (q.gate) {
-                    store8n(q.gate + m * q.N + nb + v, g, n);
-                    store8n(q.up + m * q.N + nb + v, u, n);
-                }
+        }
+    }
+    put_out<T, KIND, S>(q, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
+}
+
+// The splits' partial sums, joined in their order. FWD: both projections of
+// eight columns, then as the product's epilogue; else `batch` results.
+template <class T>
+__global__ __launch_bounds__(256) void k_gate_join_fwd(const Product q, int splits) {
+    const int per = (q.N + 7) / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / per;
+    const int n = (int)(i - m * per) * 8, left = q.N - n;
+    if (m >= q.M) return;
+    const int64_t MN = q.M * q.N, at = m * q.N + n;
+    float g[8] = {}, u[8] = {}, o[8];
+    for (int s = 0; s < splits; ++s) {
+        const Raw8<float> a = load8n(q.part + s * 2 * MN + at, left, 0.f);
+        const Raw8<float> b = load8n(q.part + (s * 2 + 1) * MN + at, left, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            g[e] += a.at(e);
+            u[e] += b.at(e);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = act_of<T>(q.act, g[e]) * u[e];
+    store8n((T*)q.out + m * q.ldo + n, o, left);
+    if (q.gate) {
+        store8n(q.gate + at, g, left);
+        store8n(q.up + at, u, left);
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_gate_join(const Product q, int splits, int batch) {
+    const int per = (q.N + 7) / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / per;
+    const int n = (int)(i - m * per) * 8, left = q.N - n, z = blockIdx.y;
+    if (m >= q.M) return;
+    const int64_t MN = q.M * q.N, at = m * q.N + n;
+    float o[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        const Raw8<float> a = load8n(q.part + (s * batch + z) * MN + at, left, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += a.at(e);
+    }
+    store8n((T*)(z ? q.out2 : q.out) + m * q.ldo + n, o, left);
+}
+
+// ---------------------------------------------------------------------------
+// The forward of a few rows: the weights' one pass through memory is all that
+// counts. A workgroup takes 16 hidden units and its four waves a quarter of the
+// summed length each; fragments go from memory to registers, without LDS, and
+// the waves' sums meet at the end.
+template <class T, int MF>
+__global__ __launch_bounds__(256) void k_gate_few(const Product q) {
+    typedef typename Mat<T>::E E;
+    typedef typename Frag<E>::V V;
+    constexpr int P = Mat<T>::P, DEEP = P == 1 ? 4 : 2;   // 32-steps under way
+    __shared__ floatx4 sum[3][2 * MF][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lk = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const int64_t per = (((q.K + 31) / 32 + 3) / 4) * 32, k0 = wave * per, k1 = min(q.K, k0 + per);
+    const int64_t n = min(n0 + li, q.N - 1);
+    const T *pg = (const T*)q.b + n * q.ldb + lk * 8, *pu = (const T*)q.b2 + n * q.ldb + lk * 8;
+    const T* px[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) px[i] = (const T*)q.a + min((int64_t)(i * 16 + li), q.M - 1) * q.lda + lk * 8;
+    floatx4 acc[2][MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) acc[0][i] = acc[1][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    auto planes = [](const Raw8<T>& r, V (&v)[P]) {
+        if constexpr (P == 1) {
+            v[0] = __builtin_bit_cast(V, r);
+        } else {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = r.at(e);
+            Raw8<bf16> c[3];
+            cut_planes(f, c);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) v[p] = __builtin_bit_cast(V, c[p]);
+        }
+    };
+    auto mma = [](const V (&b)[P], const V (&a)[P], floatx4 c) {
+        if constexpr (P == 1) return Frag<E>::mma(b[0], a[0], c);
+#pragma unroll
+        for (int t = 0; t < (P == 1 ? 0 : 6); ++t) c = Frag<E>::mma(b[kPlaneB[t] % P], a[kPlaneA[t] % P], c);
+        return c;
+    };
+    for (int64_t k = k0; k < k1; k += 32 * DEEP) {
+        Raw8<T> rg[DEEP], ru[DEEP], rx[DEEP][MF];
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            const int64_t kk = k + d * 32, left = k1 - kk - lk * 8;
+            const int c = (int)(left < 8 ? left : 8);
+            rg[d] = load8n(pg + kk, c, (T)0.f);
+            ru[d] = load8n(pu + kk, c, (T)0.f);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) rx[d][i] = load8n(px[i] + kk, c, (T)0.f);
+        }
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            V vg[P], vu[P];
+            planes(rg[d], vg);
+            planes(ru[d], vu);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                V vx[P];
+                planes(rx[d][i], vx);
+                acc[0][i] = mma(vg, vx, acc[0][i]);
+                acc[1][i] = mma(vu, vx, acc[1][i]);
+            }
+        }
+    }
+    if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            sum[wave - 1][2 * i][lane] = acc[0][i];
+            sum[wave - 1][2 * i + 1][lane] = acc[1][i];
+        }
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            acc[0][i] += sum[w][2 * i][lane];
+            acc[1][i] += sum[w][2 * i + 1][lane];
+        }
+        const int64_t m = i * 16 + li;
+        const int c = n0 + lk * 4, left = q.N - c;
+        if (m >= q.M || left <= 0) continue;
+        float g[4], u[4], o[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            g[r] = acc[0][i][r];
+            u[r] = acc[1][i][r];
+            o[r] = act_of<T>(q.act, g[r]) * u[r];
+        }
+        store4n((T*)q.out + m * q.ldo + c, o, left);
+        if (q.gate) {
+            store4n(q.gate + m * q.N + c, g, left);
+            store4n(q.up + m * q.N + c, u, left);
         }
     }
 }
@@ -387,35 +727,52 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm(const Product q) {
 // ---------------------------------------------------------------------------
 // Host side.
 
-inline int64_t up64(int64_t n) { return (n + 63) & ~int64_t(63); }
+inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// Where the operands lie in the workspace (offsets in bytes, 0 where a
-// direction does not need them).
+// Rows the forward takes without tiles.
+constexpr int64_t kFew = 32;
+
+// How a product is cut: tiles of 256 x 256 when they fill the chip, else of
+// 128 x 128, whose summed length is split when they do not fill it either
+// (two workgroups a CU), four steps or more a split.
+struct Cut {
+    bool big;
+    int mt, nt, steps, split_steps, splits;
+};
+Cut cut_of(int32_t dtype, Kind kind, int64_t M, int64_t N, int64_t K) {
+    const int bk = dtype == TT_F32 ? 32 : 64, batch = kind == DW ? 2 : 1;
+    const int64_t per = kind == FWD ? 2 : 1;   // columns of B of one of D
+    Cut c{};
+    c.steps = (int)((K + bk - 1) / bk) * (kind == DX ? 2 : 1);
+    auto tiles = [&](int64_t t) {
+        c.mt = (int)((M + t - 1) / t);
+        c.nt = (int)((N * per + t - 1) / t);
+        return (int64_t)c.mt * c.nt * batch;
+    };
+    c.big = dtype != TT_F32 && tiles(256) >= 256;
+    c.splits = 1;
+    if (!c.big) {
+        const int64_t n = tiles(128);
+        if (n > 0 && n < 256) c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(512 + n - 1) / n, c.steps / 4, 64}));
+    }
+    c.split_steps = std::max(1, (c.steps + c.splits - 1) / c.splits);
+    c.splits = std::max(1, (c.steps + c.split_steps - 1) / c.split_steps);
+    return c;
+}
+
+// Where things lie in the workspace: the backward's dg and du, then partial sums.
 struct GateSpace {
-    int64_t Kp, Hp, Mp;
-    size_t x, w, w2, forward;                 // packed operands of the forward
-    size_t gu, gut, wt, xt, backward;         // of the backward
-    GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H) {
-        const size_t e = dtype == TT_F32 ? 6 : 2;   // bytes of an element, all planes
-        Kp = up64(K);
-        Hp = up64(H);
-        Mp = up64(M);
-        size_t at = 0;
-        auto take = [&](int64_t n) {
-            const size_t o = at;
-            at += ((size_t)n * e + 255) & ~size_t(255);
-            return o;
-        };
-        x = take(M * Kp);
-        w = take(H * Kp);
-        w2 = take(H * Kp);
-        forward = at;
-        at = 0;
-        gu = take(M * 2 * Hp);
-        gut = take(2 * Hp * Mp);
-        wt = take(K * 2 * Hp);
-        xt = take(K * Mp);
-        backward = at;
+    int64_t Hp;
+    Cut fwd, dx, dw;
+    size_t part, forward, backward;   // bytes
+    GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H)
+        : Hp(up_to(H, kPanel)), fwd(cut_of(dtype, FWD, M, H, K)), dx(cut_of(dtype, DX, M, K, Hp)),
+          dw(cut_of(dtype, DW, H, K, M)) {
+        const size_t e = dtype == TT_F32 ? 4 : 2;
+        forward = M <= kFew || fwd.splits == 1 ? 0 : (size_t)fwd.splits * 2 * M * H * 4;
+        part = up_to((size_t)M * 2 * Hp * e, 256);
+        backward = part + std::max(dx.splits == 1 ? 0 : (size_t)dx.splits * M * K * 4,
+                                   dw.splits == 1 ? 0 : (size_t)dw.splits * 2 * H * K * 4);
     }
 };
 
@@ -429,114 +786,110 @@ struct GateArgs {
     hipStream_t s;
 };
 
-// Operand rows as they are, or packed into `dst`, when their alignment or
-// width does not suit the product's loads.
-template <class T>
-tt_status as_operand(Operand& o, const void* src, int64_t ld, int64_t rows, int64_t cols, char* dst, hipStream_t s) {
-    const int64_t cp = up64(cols);
-    if (Mat<T>::P == 1 && cols % kBK == 0 && ld % 8 == 0 && ((uintptr_t)src & 15) == 0) {
-        o = Operand{src, ld, 0, rows};
-        return TT_OK;
+template <class T, Kind KIND>
+tt_status product(Product q, const Cut& c, bool dma, char* part, hipStream_t s) {
+    const int batch = KIND == DW ? 2 : 1;
+    q.mt = c.mt;
+    q.nt = c.nt;
+    q.steps = c.steps;
+    q.split_steps = c.split_steps;
+    q.part = c.splits > 1 ? (float*)part : nullptr;
+    if (dma) {   // steps of 32, cut_of counts 64
+        q.steps *= 2;
+        q.split_steps *= 2;
     }
-    o = Operand{dst, cp, rows * cp, rows};
-    TT_LAUNCH(nullptr, "k_gate_pack", s, (k_gate_pack<T>), dim3(grid_for(rows * (cp / 8), 256)), dim3(256), 0, s,
-              (const T*)src, ld, rows, (int)cols, (typename Mat<T>::E*)dst, cp, rows * cp);
-    TT_LAUNCH_CHECK();
+    const bool big = c.big && dma;
+    if (c.big && !dma) {   // the tiles of the kernel for any alignment
+        q.mt = (int)((q.M + 127) / 128);
+        q.nt = (int)(((int64_t)q.N * (KIND == FWD ? 2 : 1) + 127) / 128);
+    }
+    const dim3 grid((unsigned)(q.mt * q.nt), (unsigned)c.splits, batch);
+    if constexpr (sizeof(T) == 2) {
+        if (big) {
+            TT_LAUNCH(nullptr, "k_gate_mm", s, (k_gate_mm<T, KIND, 2, 2, 8, 8>), grid, dim3(256), 0, s, q);
+        } else if (dma) {
+            TT_LAUNCH(nullptr, "k_gate_mm", s, (k_gate_mm<T, KIND, 2, 2, 4, 4>), grid, dim3(256), 0, s, q);
+        }
+        TT_LAUNCH_CHECK();
+    }
+    if (!dma) {
+        TT_LAUNCH(nullptr, "k_gate_mm_any", s, (k_gate_mm_any<T, KIND>), grid, dim3(256), 0, s, q);
+        TT_LAUNCH_CHECK();
+    }
+    if (c.splits > 1) {
+        const unsigned g = grid_for(q.M * ((q.N + 7) / 8), 256);
+        if constexpr (KIND == FWD)
+            TT_LAUNCH(nullptr, "k_gate_join_fwd", s, (k_gate_join_fwd<T>), dim3(g), dim3(256), 0, s, q, c.splits);
+        else
+            TT_LAUNCH(nullptr, "k_gate_join", s, (k_gate_join<T>), dim3(g, batch), dim3(256), 0, s, q, c.splits, batch);
+        TT_LAUNCH_CHECK();
+    }
     return TT_OK;
+}
+
+// Whether tiles can go straight to LDS: whole, aligned pieces of 16 bytes in
+// every operand that the caller lays out (hidden may be any size).
+template <class T>
+bool dma_ok(const GateArgs& a) {
+    const uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.wg | (uintptr_t)a.wu;
+    return sizeof(T) == 2 && a.K % 8 == 0 && a.ldx % 8 == 0 && (p & 15) == 0 && a.M <= (1 << 20);
 }
 
 template <class T>
-tt_status turn(const void* src, int64_t ld, int64_t rows, int64_t cols, char* dst, int64_t ldd, int64_t plane,
-               hipStream_t s) {
-    if (rows == 0) return TT_OK;
-    TT_LAUNCH(nullptr, "k_gate_turn", s, (k_gate_turn<T>), dim3(grid_for(rows, 64), grid_for(cols, 64)), dim3(256),
-              0, s, (const T*)src, ld, rows, (int)cols, (typename Mat<T>::E*)dst, ldd, plane);
-    TT_LAUNCH_CHECK();
-    return TT_OK;
-}
-
-template <class T, int EPI, int ACT>
-tt_status product(const Product& q, int z, hipStream_t s) {
-    const int nb = EPI == EPI_FWD ? 64 : 128;
-    TT_LAUNCH(nullptr, "k_gate_mm", s, (k_gate_mm<T, EPI, ACT>),
-              dim3(grid_for(q.N, nb), grid_for(q.M, 128), z), dim3(256), 0, s, q);
-    TT_LAUNCH_CHECK();
-    return TT_OK;
-}
-
-template <class T, int ACT>
 tt_status gate_forward(const GateArgs& a, const GateSpace& sp) {
     Product q{};
-    tt_status st = as_operand<T>(q.a, a.x, a.ldx, a.M, a.K, a.ws + sp.x, a.s);
-    if (st == TT_OK) st = as_operand<T>(q.b, a.wg, a.K, a.H, a.K, a.ws + sp.w, a.s);
-    if (st == TT_OK) st = as_operand<T>(q.b2, a.wu, a.K, a.H, a.K, a.ws + sp.w2, a.s);
-    if (st != TT_OK) return st;
-    q.M = a.M;
-    q.N = (int)a.H;
-    q.kp = (int)sp.Kp;
-    q.out = a.out;
-    q.ldo = a.ldout;
-    q.gate = a.gate;
-    q.up = a.up;
-    return product<T, EPI_FWD, ACT>(q, 1, a.s);
-}
-
-template <class T, int ACT>
-tt_status gate_backward(const GateArgs& a, const GateSpace& sp) {
-    typedef typename Mat<T>::E E;
-    const int64_t gu_plane = a.M * 2 * sp.Hp, gut_plane = 2 * sp.Hp * sp.Mp, wt_plane = a.K * 2 * sp.Hp,
-                  xt_plane = a.K * sp.Mp;
-    E *gu = (E*)(a.ws + sp.gu), *gut = (E*)(a.ws + sp.gut);
-    char *wt = a.ws + sp.wt, *xt = a.ws + sp.xt;
-    tt_status st = turn<T>(a.x, a.ldx, a.M, a.K, xt, sp.Mp, xt_plane, a.s);
-    if (a.M > 0) {
-        TT_LAUNCH(nullptr, "k_gate_grad", a.s, (k_gate_grad<T, ACT>), dim3(grid_for(a.M, 64), grid_for(a.H, 64)),
-                  dim3(256), 0, a.s, a.gate, a.up, (const T*)a.dout, a.lddout, a.M, (int)a.H, (int)sp.Hp, sp.Mp, gu,
-                  gu_plane, gut, gut_plane);
+    q.a = a.x; q.b = a.wg; q.b2 = a.wu;
+    q.lda = a.ldx; q.ldb = a.K;
+    q.pa = q.pb = kPanel;
+    q.bytes_a = ((a.M - 1) * a.ldx + a.K) * (int64_t)sizeof(T);
+    q.bytes_b = a.H * a.K * (int64_t)sizeof(T);
+    q.M = a.M; q.N = (int)a.H; q.K = a.K;
+    q.out = a.out; q.ldo = a.ldout;
+    q.gate = a.gate; q.up = a.up; q.act = a.act;
+    if (a.M <= kFew) {
+        auto k = a.M <= 16 ? k_gate_few<T, 1> : k_gate_few<T, 2>;
+        TT_LAUNCH(nullptr, "k_gate_few", a.s, k, dim3(grid_for(a.H, 16)), dim3(256), 0, a.s, q);
         TT_LAUNCH_CHECK();
-        // the turned weights side by side: [K][Hp of Wg | Hp of Wu]
-        if (st == TT_OK) st = turn<T>(a.wg, a.K, a.H, a.K, wt, 2 * sp.Hp, wt_plane, a.s);
-        if (st == TT_OK) st = turn<T>(a.wu, a.K, a.H, a.K, wt + sp.Hp * 2, 2 * sp.Hp, wt_plane, a.s);
-        Product q{};
-        q.a = Operand{gu, 2 * sp.Hp, gu_plane, a.M};
-        q.b = Operand{wt, 2 * sp.Hp, wt_plane, a.K};
-        q.M = a.M;
-        q.N = (int)a.K;
-        q.kp = (int)(2 * sp.Hp);
-        q.out = a.dx;
-        q.ldo = a.lddx;
-        if (st == TT_OK) st = product<T, EPI_OUT, 0>(q, 1, a.s);
+        return TT_OK;
     }
-    if (st != TT_OK) return st;
-    Product q{};
-    q.a = Operand{gut, sp.Mp, gut_plane, sp.Hp};
-    q.b = Operand{xt, sp.Mp, xt_plane, a.K};
-    q.M = a.H;
-    q.N = (int)a.K;
-    q.kp = (int)sp.Mp;
-    q.out = a.dwg;
-    q.out2 = a.dwu;
-    q.ldo = a.K;
-    return product<T, EPI_OUT, 0>(q, 2, a.s);
-}
-
-template <class T, int ACT>
-tt_status gate_run(const GateArgs& a, const GateSpace& sp, bool backward) {
-    return backward ? gate_backward<T, ACT>(a, sp) : gate_forward<T, ACT>(a, sp);
+    return product<T, FWD>(q, sp.fwd, dma_ok<T>(a), a.ws, a.s);
 }
 
 template <class T>
-tt_status gate_by_act(const GateArgs& a, const GateSpace& sp, bool backward) {
-    if (a.act == TT_ACT_SILU) return gate_run<T, TT_ACT_SILU>(a, sp, backward);
-    if (a.act == TT_ACT_GELU) return gate_run<T, TT_ACT_GELU>(a, sp, backward);
-    return gate_run<T, TT_ACT_RELU>(a, sp, backward);
+tt_status gate_backward(const GateArgs& a, const GateSpace& sp) {
+    T* gu = (T*)a.ws;
+    Product q{};
+    const bool dma = dma_ok<T>(a);
+    const int panel = dma ? kPanel : (int)sp.Hp;
+    q.a = gu;
+    q.lda = panel;
+    q.pa = dma ? a.M * kPanel : kPanel;
+    q.pb = kPanel;
+    q.a2 = a.M * sp.Hp;
+    q.bytes_a = a.M * 2 * sp.Hp * (int64_t)sizeof(T);
+    if (a.M > 0) {
+        TT_LAUNCH(nullptr, "k_gate_grad", a.s, (k_gate_grad<T>), dim3(grid_for(a.M * (sp.Hp / 8), 256)), dim3(256), 0,
+                  a.s, a.gate, a.up, (const T*)a.dout, a.lddout, a.M, (int)a.H, (int)sp.Hp, panel, a.act, gu);
+        TT_LAUNCH_CHECK();
+        q.b = a.wg; q.b2 = a.wu; q.ldb = a.K;
+        q.bytes_b = a.H * a.K * (int64_t)sizeof(T);
+        q.M = a.M; q.N = (int)a.K; q.K = a.H;
+        q.out = a.dx; q.ldo = a.lddx;
+        const tt_status st = product<T, DX>(q, sp.dx, dma, a.ws + sp.part, a.s);
+        if (st != TT_OK) return st;
+    }
+    q.b = a.x; q.b2 = nullptr; q.ldb = a.ldx;
+    q.bytes_b = ((a.M - 1) * a.ldx + a.K) * (int64_t)sizeof(T);
+    q.M = a.H; q.N = (int)a.K; q.K = a.M;
+    q.out = a.dwg; q.out2 = a.dwu; q.ldo = a.K;
+    return product<T, DW>(q, sp.dw, dma, a.ws + sp.part, a.s);
 }
 
 tt_status gate_by_type(int32_t dtype, const GateArgs& a, bool backward) {
     const GateSpace sp(dtype, a.M, a.K, a.H);
-    if (dtype == TT_F32) return gate_by_act<float>(a, sp, backward);
-    if (dtype == TT_BF16) return gate_by_act<bf16>(a, sp, backward);
-    return gate_by_act<f16>(a, sp, backward);
+    if (dtype == TT_F32) return backward ? gate_backward<float>(a, sp) : gate_forward<float>(a, sp);
+    if (dtype == TT_BF16) return backward ? gate_backward<bf16>(a, sp) : gate_forward<bf16>(a, sp);
+    return backward ? gate_backward<f16>(a, sp) : gate_forward<f16>(a, sp);
 }
 
 constexpr int64_t kGateMaxWidth = 1 << 20;

@@ -89,7 +89,21 @@ __device__ __forceinline__ void store8n(T* __restrict__ p, const float (&f)[8], 
         if (e < n) p[e] = (T)f[e];
 }
 
-// The same, past the caches.
+template <class T>
+__device__ __forceinline__ void store4n(T* __restrict__ p, const float (&f)[4], int n) {
+    if (n >= 4) {
+        struct alignas(8) {
+            T v[4];
+        } r = {(T)f[0], (T)f[1], (T)f[2], (T)f[3]};
+        __builtin_memcpy(p, &r, sizeof(r));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n) p[e] = (T)f[e];
+}
+
+// Eight, past the caches.
 template <class T>
 __device__ __forceinline__ void store8n_apart(T* __restrict__ p, const float (&f)[8], int n) {
     if (n < 8) return store8n(p, f, n);

@@ -210,6 +210,13 @@ def test_gate_larger(dt):
     check_gate(*gate_inputs(2100, 512, 1300, dt), "silu")
 
 
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("m,k,h", [(4200, 4104, 2100), (4100, 2056, 4200)])
+def test_gate_large_tiles(dt, m, k, h):
+    """Sizes that fill the chip with the largest tiles, none a multiple of them."""
+    check_gate(*gate_inputs(m, k, h, dt), "silu")
+
+
 def test_gate_fp32_range():
     """fp32 operands keep their range: products of very large and very small values."""
     x, wg, wu, d = gate_inputs(70, 128, 64, F32)
