@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
 //
 // By rows: ROWS rows of BK elements; a row's 16-byte pieces are stored in the
 // order piece ^ key(row), so that the rows that lanes read together lie in
-// different banks.
+// different banks: consecutive ones for GROUP = 4, else r..r+3, r + GROUP...
 //
 // By columns: BK rows (the summed index k) of ROWS elements; a row's 32-byte
 // blocks are stored in the order block ^ (k & 3 | k >> 3 & 1): the transposing
@@ -160,27 +160,28 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
 // [line][kPanel]. A step's tile by rows is then one piece of memory.
 constexpr int kPanel = 32;
 
-template <int BK>
+template <int BK, int GROUP>
 __device__ __forceinline__ int row_slot(int row, int piece) {
-    return piece ^ (BK == 64 ? row & 7 : (row >> 1) & 3);
+    if (BK == 64) return piece ^ ((row & 3) | (((row / GROUP) & 1) << 2));
+    return piece ^ (((row >> 1) & 1) | (((row / GROUP) & 1) << 1));
 }
 __device__ __forceinline__ int col_key(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
 // Byte offset of 16-byte piece `piece` of line `line` (a row, or a k).
-template <bool COLS, int BK, int ROWS>
+template <bool COLS, int BK, int ROWS, int GROUP>
 __device__ __forceinline__ int lds_piece(int line, int piece) {
     if (COLS) return line * (ROWS * 2) + ((piece >> 1) ^ col_key(line)) * 32 + (piece & 1) * 16;
-    return line * (BK * 2) + row_slot<BK>(line, piece) * 16;
+    return line * (BK * 2) + row_slot<BK, GROUP>(line, piece) * 16;
 }
 
 // The fragment of 16 rows (or columns) x 32 k, k in [32 h, 32 h + 32): lane l
 // holds 8 consecutive k, from 8 (l / 16), of its row. By rows the lane's row
 // is `row`; by columns the fragment's columns are row0 + 0..15.
-template <class V, bool COLS, int BK, int ROWS>
+template <class V, bool COLS, int BK, int ROWS, int GROUP>
 __device__ __forceinline__ V fragment(const char* lds, int row, int row0, int h) {
     const int lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
     if constexpr (!COLS) {
-        return *reinterpret_cast<const V*>(lds + lds_piece<false, BK, ROWS>(row, h * 4 + lk));
+        return *reinterpret_cast<const V*>(lds + lds_piece<false, BK, ROWS, GROUP>(row, h * 4 + lk));
     } else {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -231,51 +232,63 @@ __device__ __forceinline__ void tile_of(const Product& q, int& tm, int& tn) {
     tn = in / rows;
 }
 
-// A tile's loads straight to LDS, 16 bytes a lane and 1024 an instruction. The
-// buffer descriptor starts at the tile's first line of the step and ends with
-// the operand, past which the loads deliver zeros. What lies past the summed
-// length is given an offset outside the buffer, for zeros too. (Lines and pieces
-// past the last row or column of D may read what follows in the operand; their
-// results are dropped.)
-template <bool COLS, int BK, int ROWS, int WAVES>
+// A tile's loads straight to LDS, 16 bytes a lane and 1024 an instruction. A
+// lane's offsets within the tile stay; the buffer descriptor's base moves along
+// the summed index. Rows and pieces past the operand's last are read as the
+// last (their results are dropped); what lies past the summed length is given
+// an offset outside the buffer, for which the load delivers zeros.
+template <bool COLS, int BK, int ROWS, int GROUP, int WAVES>
 struct DmaLoad {
     static constexpr int N = ROWS * BK * 2 / 1024 / WAVES;    // instructions of a wave
     static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;   // of a line
     static constexpr int LINES = 64 / PIECES;                 // of an instruction
-    uint32_t off[N];   // of this lane's piece from the instruction's first line
-    uint32_t line;     // bytes from line to line
+    uint32_t off[N];
     int wave;
+    __device__ __forceinline__ int line(int i) const { return (wave * N + i) * LINES + (threadIdx.x & 63) / PIECES; }
     __device__ __forceinline__ int piece(int i) const {
-        const int lane = threadIdx.x & 63, l = (wave * N + i) * LINES + lane / PIECES, s = lane % PIECES;
-        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot<BK>(l, s);
+        const int l = line(i), s = (threadIdx.x & 63) % PIECES;
+        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot<BK, GROUP>(l, s);
     }
-    __device__ __forceinline__ void init(int64_t ld, int64_t panel) {
-        line = (uint32_t)ld * 2;
+    // ld, panel: elements from line to line and from panel to panel; row0: the
+    // tile's first row (column) of `rows`
+    __device__ __forceinline__ void init(int64_t ld, int64_t panel, int64_t row0, int64_t rows) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int64_t last = rows - 1 - row0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int p = piece(i);
-            off[i] = (threadIdx.x & 63) / PIECES * line + p / (kPanel / 8) * (uint32_t)panel * 2 + p % (kPanel / 8) * 16;
+            int l = line(i), p = piece(i);
+            if (COLS) p = p < last / 8 ? p : (int)(last / 8);
+            else l = l < last ? l : (int)last;
+            off[i] = (uint32_t)((l * ld + p / (kPanel / 8) * panel) * 2 + p % (kPanel / 8) * 16);
         }
     }
-    // Instruction i. base: the tile's first line at this step; bytes: from there
-    // to the operand's end; left: of the summed length
-    __device__ __forceinline__ void load(int i, char* lds, const char* base, int64_t bytes, int64_t left) const {
+    // Instruction i. base: the tile's first line at this step; left: of the
+    // summed length
+    __device__ __forceinline__ void load(int i, char* lds, const char* base, int left) const {
 #ifdef __HIP_DEVICE_COMPILE__   // the descriptor's type is the device compiler's
-        const int n = left < BK ? (int)left : BK;
-        const int64_t size = left <= 0 || bytes < 0 ? 0 : bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF;
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)size, 0x00020000);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7FFFFFFF, 0x00020000);
+        const uint32_t o = (COLS ? line(i) : piece(i) * 8) < left ? off[i] : 0x80000000u;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * N + i) * 1024), 16,
-            (COLS ? (wave * N + i) * LINES + (int)(threadIdx.x & 63) / PIECES : piece(i) * 8) < n ? off[i] : 0x80000000u,
-            (wave * N + i) * LINES * line, 0, 0);
+            rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * N + i) * 1024), 16, o, 0, 0, 0);
 #endif
     }
 };
 
+// Lambdas of the product's step are part of it, whatever their size.
+#define TT_INLINE __attribute__((always_inline))
+
+// f(0), .., f(N - 1) with constant arguments.
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<N, F, I + 1>(f);
+    }
+}
+
 // The same tile through registers: any alignment, and fp32, cut into planes on
 // its way to LDS.
-template <class T, bool COLS, int BK, int ROWS, int THREADS>
+template <class T, bool COLS, int BK, int ROWS, int GROUP, int THREADS>
 struct RegLoad {
     static constexpr int P = Mat<T>::P, N = ROWS * BK / 8 / THREADS;
     static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;
@@ -294,7 +307,7 @@ struct RegLoad {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int id = i * THREADS + threadIdx.x, line = id / PIECES, piece = id % PIECES;
-            char* q = lds + lds_piece<COLS, BK, ROWS>(line, piece);
+            char* q = lds + lds_piece<COLS, BK, ROWS, GROUP>(line, piece);
             if constexpr (P == 1) {
                 *reinterpret_cast<Raw8<T>*>(q) = r[i];
             } else {
@@ -318,10 +331,18 @@ struct Shape {
     static constexpr int FH = KIND == FWD ? FN / 2 : FN;  // fragments of D's columns in a wave
     static constexpr int NB = KIND == FWD ? TN / 2 : TN;  // columns of D of a workgroup
     // (FWD: LDS rows [0, NB) of B are Wg's, [NB, TN) Wu's, and so are a wave's fragments)
+    // Columns of D that a lane ends up with side by side: in FWD a wave's FH fragments
+    // interleave, for stores of 16 bytes.
+    static constexpr int GROUP = KIND == FWD ? 4 * FH : 4;
+    // The row of B's tile, from the wave's first one, that is row i of fragment x.
+    static __device__ __forceinline__ int row_of(int x, int i) {
+        return KIND == FWD ? (i >> 2) * GROUP + x % FH * 4 + (i & 3) : x * 16 + i;
+    }
 };
 
-// Results of a wave. acc[i][j][r] is D[m][n], m = i * 16 + lane % 16 and
-// n = j * 16 + lane / 16 * 4 + r; in FWD g for j < FH, and u FH fragments on.
+// Results of a wave: acc[i][j][r] is D[m][n], m = i * 16 + lane % 16 and
+// n = j * 16 + lane / 16 * 4 + r. In FWD it is g for j < FH, u FH fragments on,
+// with n consecutive over (j, r) from lane / 16 * GROUP on.
 template <class T, Kind KIND, class S, int FM, int FN>
 __device__ __forceinline__ void put_out(const Product& q, const floatx4 (&acc)[FM][FN], int64_t m0, int n0) {
     const int li = threadIdx.x & 15, lk = (threadIdx.x & 63) >> 4;
@@ -331,32 +352,40 @@ __device__ __forceinline__ void put_out(const Product& q, const floatx4 (&acc)[F
         __builtin_amdgcn_sched_barrier(0);   // row by row: no registers for several at once
         const int64_t m = m0 + i * 16 + li;
         if (m >= q.M) continue;
+        if constexpr (KIND == FWD) {
 #pragma unroll
-        for (int j = 0; j < S::FH; ++j) {
-            const int n = n0 + j * 16 + lk * 4, left = q.N - n;
-            if (left <= 0) continue;
-            const float d[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            if constexpr (KIND == FWD) {
-                const floatx4 v = acc[i][j + S::FH];
-                const float u[4] = {v[0], v[1], v[2], v[3]};
+            for (int v = 0; v < S::GROUP; v += 8) {
+                const int n = n0 + lk * S::GROUP + v, left = q.N - n;
+                if (left <= 0) continue;
+                float g[8], u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    g[e] = acc[i][(v + e) / 4][e & 3];
+                    u[e] = acc[i][(v + e) / 4 + S::FH][e & 3];
+                }
                 float *pg = q.gate, *pu = q.up;
                 if (q.part) {
                     pg = q.part + blockIdx.y * 2 * MN;
                     pu = pg + MN;
                 } else {
-                    float o[4];
+                    float o[8];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = act_of<T>(q.act, d[r]) * u[r];
-                    store4n((T*)q.out + m * q.ldo + n, o, left);
+                    for (int e = 0; e < 8; ++e) o[e] = act_of<T>(q.act, g[e]) * u[e];
+                    store8n((T*)q.out + m * q.ldo + n, o, left);
                 }
                 if (pg) {
-                    store4n(pg + m * q.N + n, d, left);
-                    store4n(pu + m * q.N + n, u, left);
+                    store8n(pg + m * q.N + n, g, left);
+                    store8n(pu + m * q.N + n, u, left);
                 }
-            } else if (q.part) {
-                store4n(q.part + (blockIdx.y * gridDim.z + blockIdx.z) * MN + m * q.N + n, d, left);
-            } else {
-                store4n((T*)(blockIdx.z ? q.out2 : q.out) + m * q.ldo + n, d, left);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int n = n0 + j * 16 + lk * 4, left = q.N - n;
+                if (left <= 0) continue;
+                const float d[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                if (q.part) store4n(q.part + (blockIdx.y * gridDim.z + blockIdx.z) * MN + m * q.N + n, d, left);
+                else store4n((T*)(blockIdx.z ? q.out2 : q.out) + m * q.ldo + n, d, left);
             }
         }
     }
@@ -373,24 +402,14 @@ __device__ __forceinline__ void landed_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// acc[j] += b[j] a for a row of fragments, in place in the accumulation
-// registers. (With all 256 of them in use the compiler's own choice moves
-// accumulators to and fro, 100 moves a step.) The leading wait covers operands
-// that a vector instruction has just written.
-template <class T, class V, int FN>
-__device__ __forceinline__ void mma_row(floatx4 (&c)[FN], const V& a, const V (&b)[FN]) {
-    static_assert(FN == 4 || FN == 8, "fragments of a row");
-#define TT_MMA4(OP, J)                                                                                       \
-    asm volatile("s_nop 1\n\t" OP " %0, %4, %8, %0\n\t" OP " %1, %5, %8, %1\n\t" OP " %2, %6, %8, %2\n\t" OP \
-                 " %3, %7, %8, %3"                                                                           \
-                 : "+a"(c[J]), "+a"(c[J + 1]), "+a"(c[J + 2]), "+a"(c[J + 3])                                \
-                 : "v"(b[J]), "v"(b[J + 1]), "v"(b[J + 2]), "v"(b[J + 3]), "v"(a))
-#pragma unroll
-    for (int j = 0; j < FN; j += 4) {
-        if constexpr (std::is_same<T, bf16>::value) TT_MMA4("v_mfma_f32_16x16x32_bf16", j);
-        else TT_MMA4("v_mfma_f32_16x16x32_f16", j);
-    }
-#undef TT_MMA4
+// c += b a, in place in the accumulation registers. (With all 256 of them in use
+// the compiler's own choice moves accumulators to and fro, 100 moves a step.)
+template <class T, class V>
+__device__ __forceinline__ void mma_in_place(floatx4& c, const V& a, const V& b) {
+    if constexpr (std::is_same<T, bf16>::value)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+    else
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
 }
 
 // Waits until the matrix instructions' results can be read: 32 cycles, tied to
@@ -424,24 +443,43 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
     const int n0 = tn * S::NB;
     const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
 
-    DmaLoad<S::AC, BK, S::TM, WAVES> la;
-    DmaLoad<S::BC, BK, S::NB, WAVES> lb;
-    la.init(q.lda, q.pa);
-    lb.init(q.ldb, q.pb);
+    DmaLoad<S::AC, BK, S::TM, 4, WAVES> la;
+    DmaLoad<S::BC, BK, S::NB, S::GROUP, WAVES> lb;
+    la.init(q.lda, q.pa, m0, q.M);
+    lb.init(q.ldb, q.pb, n0, q.N);
     constexpr int LOADS = la.N + lb.N * (KIND == FWD ? 2 : 1);   // a wave's a step
     static_assert(BK == kPanel && S::TM % kPanel == 0 && S::NB % kPanel == 0, "tiles are whole panels");
     const int64_t ta = (S::AC ? m0 / kPanel * q.pa : m0 * q.lda) * 2 + (KIND == DW ? (int64_t)blockIdx.z * q.a2 * 2 : 0);
     const int64_t tb = (S::BC ? n0 / kPanel * q.pb : n0 * q.ldb) * 2;
+    const int64_t da = (S::AC ? BK * q.lda : q.pa) * 2, db = (S::BC ? BK * q.ldb : q.pb) * 2;   // from step to step
+    // DX: the steps of dg and Wg, then those of du and Wu
     const int half = KIND == DX ? q.steps / 2 : q.steps;
-    // load x of a step; steps past the last one are zeros
-    auto load = [&](char* sa, char* sb, int step, int x) {
+    const char *first_a, *first_b, *first_b2;   // of the step that is loaded next
+    int left;                                   // of the summed length there; 0 past the last step
+    auto start = [&](int step) TT_INLINE {
         const bool second = KIND == DX && step >= half;
-        const int64_t k = (int64_t)(second ? step - half : step) * BK, left = step < s1 ? q.K - k : 0;
-        const int64_t oa = ta + (S::AC ? k * q.lda : k / kPanel * q.pa + (second ? q.a2 : 0)) * 2;
-        const int64_t ob = tb + (S::BC ? k * q.ldb : k / kPanel * q.pb) * 2;
-        if (x < la.N) la.load(x, sa, (const char*)q.a + oa, q.bytes_a - oa, left);
-        else if (x < la.N + lb.N) lb.load(x - la.N, sb, (const char*)(second ? q.b2 : q.b) + ob, q.bytes_b - ob, left);
-        else if (KIND == FWD) lb.load(x - la.N - lb.N, sb + S::NB * BK * 2, (const char*)q.b2 + ob, q.bytes_b - ob, left);
+        const int64_t k = second ? step - half : step;
+        first_a = (const char*)q.a + ta + k * da + (second ? q.a2 * 2 : 0);
+        first_b = (const char*)(second ? q.b2 : q.b) + tb + k * db;
+        first_b2 = (const char*)q.b2 + tb + k * db;
+        left = (int)(q.K - k * BK);
+    };
+    auto advance = [&](int step) TT_INLINE {   // to `step`
+        if (KIND == DX && step == half) {
+            start(step);
+        } else {
+            first_a += da;
+            first_b += db;
+            if (KIND == FWD) first_b2 += db;
+            left -= BK;
+        }
+        if (step >= s1) left = 0;
+    };
+    // load x of the step that is loaded next
+    auto load = [&](char* sa, char* sb, int x) TT_INLINE {
+        if (x < la.N) la.load(x, sa, first_a, left);
+        else if (x < la.N + lb.N) lb.load(x - la.N, sb, first_b, left);
+        else lb.load(x - la.N - lb.N, sb + S::NB * BK * 2, first_b2, left);
     };
 
     floatx4 acc[FM][FN];
@@ -452,43 +490,46 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
 
     // fragment x of a step: B's first, which every row of products needs, then A's
     V f0[FN + FM], f1[FN + FM];
-    auto read = [&](V (&f)[FN + FM], const char* sa, const char* sb, int x) {
+    auto read = [&](V (&f)[FN + FM], const char* sa, const char* sb, int x) TT_INLINE {
         if (x < FN) {
-            const int w = (wn * S::FH + x % S::FH) * 16;
-            f[x] = fragment<V, S::BC, BK, S::NB>(sb + x / S::FH * S::NB * BK * 2, w + li, w, 0);
+            const int w = wn * S::FH * 16;
+            f[x] = fragment<V, S::BC, BK, S::NB, S::GROUP>(sb + x / S::FH * S::NB * BK * 2, w + S::row_of(x, li),
+                                                           w + x * 16, 0);
         } else {
             const int r = wm * FM * 16 + (x - FN) * 16;
-            f[x] = fragment<V, S::AC, BK, S::TM>(sa, r + li, r, 0);
+            f[x] = fragment<V, S::AC, BK, S::TM, 4>(sa, r + li, r, 0);
         }
     };
     // Step s: products of its fragments f; fragments g of step s + 1 from (ta, tb), early enough
     // that the last arrive before they are needed; loads of step s + 4 into (sa, sb), step s's own.
-    auto step = [&](int s, V (&f)[FN + FM], V (&g)[FN + FM], char* sa, char* sb, const char* ta, const char* tb) {
+    // A matrix instruction takes 16 cycles, in which a wave can issue three others: reads and loads
+    // stand one by one between them, never together.
+    auto step = [&](int s, V (&f)[FN + FM], V (&g)[FN + FM], char* sa, char* sb, const char* ta,
+                    const char* tb) TT_INLINE {
         landed_barrier<2 * LOADS>();   // step s + 1 is there, s + 2 and s + 3 may be under way
-        constexpr int PER = (FN + FM + FM - 2) / (FM - 1);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-#pragma unroll
-            for (int x = i * PER; x < (i + 1) * PER && x < FN + FM; ++x) read(g, ta, tb, x);
-#pragma unroll
-            for (int x = i * LOADS / FM; x < (i + 1) * LOADS / FM; ++x) load(sa, sb, s + 4, x);
-            mma_row<T>(acc[i], f[FN + i], reinterpret_cast<const V(&)[FN]>(f));
+        constexpr int SLOTS = FM * FN, READ = SLOTS - FN;
+        each<SLOTS>([&](auto slot) TT_INLINE {
+            constexpr int t = slot;
             __builtin_amdgcn_sched_barrier(0);
-        }
+            mma_in_place<T>(acc[t / FN][t % FN], f[FN + t / FN], f[t % FN]);
+            if constexpr (t < READ)
+                each<(t + 1) * (FN + FM) / READ - t * (FN + FM) / READ>(
+                    [&](auto x) TT_INLINE { read(g, ta, tb, t * (FN + FM) / READ + x); });
+            each<LOADS>([&](auto x) TT_INLINE {
+                if constexpr (t == (2 * x + 1) * SLOTS / (2 * LOADS)) load(sa, sb, x);
+            });
+        });
+        advance(s + 5);
     };
-
     if (s0 < s1) {
-#pragma unroll
-        for (int x = 0; x < LOADS; ++x) load(sa0, sb0, s0, x);
-#pragma unroll
-        for (int x = 0; x < LOADS; ++x) load(sa1, sb1, s0 + 1, x);
-#pragma unroll
-        for (int x = 0; x < LOADS; ++x) load(sa2, sb2, s0 + 2, x);
-#pragma unroll
-        for (int x = 0; x < LOADS; ++x) load(sa3, sb3, s0 + 3, x);
+        start(s0);
+        each<4>([&](auto d) TT_INLINE {
+            char *sa = d == 0 ? sa0 : d == 1 ? sa1 : d == 2 ? sa2 : sa3, *sb = d == 0 ? sb0 : d == 1 ? sb1 : d == 2 ? sb2 : sb3;
+            each<LOADS>([&](auto x) TT_INLINE { load(sa, sb, x); });
+            advance(s0 + d + 1);
+        });
         landed_barrier<3 * LOADS>();
-#pragma unroll
-        for (int x = 0; x < FN + FM; ++x) read(f0, sa0, sb0, x);
+        each<FN + FM>([&](auto x) TT_INLINE { read(f0, sa0, sb0, x); });
         for (int s = s0; s < s1; s += 4) {   // up to three steps of zeros at the end
             step(s, f0, f1, sa0, sb0, sa1, sb1);
             step(s + 1, f1, f0, sa1, sb1, sa2, sb2);
@@ -521,8 +562,8 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
     const int n0 = tn * S::NB;
     const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
 
-    RegLoad<T, S::AC, BK, S::TM, 256> la;
-    RegLoad<T, S::BC, BK, S::NB, 256> lb, lb2;
+    RegLoad<T, S::AC, BK, S::TM, 4, 256> la;
+    RegLoad<T, S::BC, BK, S::NB, S::GROUP, 256> lb, lb2;
     const T* pa = (const T*)q.a + (KIND == DW ? (int64_t)blockIdx.z * q.a2 : 0);
     const int half = KIND == DX ? q.steps / 2 : q.steps;
     auto load = [&](int step) {
@@ -555,15 +596,16 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     const int r = wm * FM * 16 + i * 16;
-                    fa[p][i] = fragment<V, S::AC, BK, S::TM>(sa + p * PA, r + li, r, h);
+                    fa[p][i] = fragment<V, S::AC, BK, S::TM, 4>(sa + p * PA, r + li, r, h);
                 }
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 V fb[P];
-                const int w = (wn * S::FH + j % S::FH) * 16;
+                const int w = wn * S::FH * 16;
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    fb[p] = fragment<V, S::BC, BK, S::NB>(sb + (j / S::FH * P + p) * PB, w + li, w, h);
+                    fb[p] = fragment<V, S::BC, BK, S::NB, S::GROUP>(sb + (j / S::FH * P + p) * PB,
+                                                                    w + S::row_of(j, li), w + j * 16, h);
                 if constexpr (P == 1) {
 #pragma unroll
                     for (int i = 0; i < FM; ++i) acc[i][j] = Frag<E>::mma(fb[0], fa[0][i], acc[i][j]);
