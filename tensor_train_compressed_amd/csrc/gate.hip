@@ -116,18 +116,22 @@ __device__ __forceinline__ void act_grad(int act, float g, float& a, float& da) 
 }
 
 // ---------------------------------------------------------------------------
-// dg and du, into gu [2][Hp / panel][M][panel] (Hp: H up to a multiple of kPanel,
-// zeros past H; panel: Hp for plain rows, or kPanel).
+// Elements of a line that lie together in an operand cut into panels: [panel]
+// [line][kPanel]. A step's tile by rows is then one piece of memory.
+constexpr int kPanel = 32;
 
+// dg and du, into gu [2][Hp / panel][M][panel] (Hp: H up to a multiple of kPanel,
+// zeros past H; panel: Hp for plain rows, or kPanel). A wave takes 16 rows of 32
+// elements, which it reads as whole cache lines and writes as one piece.
+// Bound by memory: 8192 x 10240, 1.2 GB in GRAD_US us.
 template <class T>
 __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gate, const float* __restrict__ up,
                                                    const T* __restrict__ dout, int64_t ldo, int64_t M, int H, int Hp,
                                                    int panel, int act, T* __restrict__ gu) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int per = Hp / 8;
-    const int64_t m = i / per;
-    const int h = (int)(i - m * per) * 8, n = H - h;
-    if (m >= M) return;
+    const int quads = (Hp / kPanel + 3) / 4;   // workgroups along a row
+    const int64_t m = blockIdx.x / quads * 16 + (threadIdx.x & 63) / 4;
+    const int h = (blockIdx.x % quads * 4 + threadIdx.x / 64) * kPanel + (threadIdx.x & 3) * 8, n = H - h;
+    if (m >= M || h >= Hp) return;
     const Raw8<float> g = load8n(gate + m * H + h, n, 0.f), u = load8n(up + m * H + h, n, 0.f);
     const Raw8<T> d = load8n(dout + m * ldo + h, n, (T)0.f);
     float dg[8], du[8];
@@ -139,7 +143,7 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
         dg[e] = e < n ? o * u.at(e) * da : 0.f;
         du[e] = e < n ? o * a : 0.f;
     }
-    T* p = gu + (h / panel * M + m) * panel + h % panel;
+    T* p = panel == kPanel ? gu + (h / kPanel * M + m) * kPanel + h % kPanel : gu + m * panel + h;
     store8n(p, dg, 8);
     store8n(p + M * Hp, du, 8);
 }
@@ -149,39 +153,34 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
 //
 // By rows: ROWS rows of BK elements; a row's 16-byte pieces are stored in the
 // order piece ^ key(row), so that the rows that lanes read together lie in
-// different banks: consecutive ones for GROUP = 4, else r..r+3, r + GROUP...
+// different banks.
 //
 // By columns: BK rows (the summed index k) of ROWS elements; a row's 32-byte
 // blocks are stored in the order block ^ (k & 3 | k >> 3 & 1): the transposing
 // load of 16 lanes takes 32 bytes of four rows k, and four such groups are 8
 // rows apart.
 
-// Elements of a line that lie together in an operand cut into panels: [panel]
-// [line][kPanel]. A step's tile by rows is then one piece of memory.
-constexpr int kPanel = 32;
-
-template <int BK, int GROUP>
+template <int BK>
 __device__ __forceinline__ int row_slot(int row, int piece) {
-    if (BK == 64) return piece ^ ((row & 3) | (((row / GROUP) & 1) << 2));
-    return piece ^ (((row >> 1) & 1) | (((row / GROUP) & 1) << 1));
+    return piece ^ (BK == 64 ? row & 7 : (row >> 1) & 3);
 }
 __device__ __forceinline__ int col_key(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
 // Byte offset of 16-byte piece `piece` of line `line` (a row, or a k).
-template <bool COLS, int BK, int ROWS, int GROUP>
+template <bool COLS, int BK, int ROWS>
 __device__ __forceinline__ int lds_piece(int line, int piece) {
     if (COLS) return line * (ROWS * 2) + ((piece >> 1) ^ col_key(line)) * 32 + (piece & 1) * 16;
-    return line * (BK * 2) + row_slot<BK, GROUP>(line, piece) * 16;
+    return line * (BK * 2) + row_slot<BK>(line, piece) * 16;
 }
 
 // The fragment of 16 rows (or columns) x 32 k, k in [32 h, 32 h + 32): lane l
 // holds 8 consecutive k, from 8 (l / 16), of its row. By rows the lane's row
 // is `row`; by columns the fragment's columns are row0 + 0..15.
-template <class V, bool COLS, int BK, int ROWS, int GROUP>
+template <class V, bool COLS, int BK, int ROWS>
 __device__ __forceinline__ V fragment(const char* lds, int row, int row0, int h) {
     const int lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
     if constexpr (!COLS) {
-        return *reinterpret_cast<const V*>(lds + lds_piece<false, BK, ROWS, GROUP>(row, h * 4 + lk));
+        return *reinterpret_cast<const V*>(lds + lds_piece<false, BK, ROWS>(row, h * 4 + lk));
     } else {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -237,7 +236,7 @@ __device__ __forceinline__ void tile_of(const Product& q, int& tm, int& tn) {
 // the summed index. Rows and pieces past the operand's last are read as the
 // last (their results are dropped); what lies past the summed length is given
 // an offset outside the buffer, for which the load delivers zeros.
-template <bool COLS, int BK, int ROWS, int GROUP, int WAVES>
+template <bool COLS, int BK, int ROWS, int WAVES>
 struct DmaLoad {
     static constexpr int N = ROWS * BK * 2 / 1024 / WAVES;    // instructions of a wave
     static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;   // of a line
@@ -247,7 +246,7 @@ struct DmaLoad {
     __device__ __forceinline__ int line(int i) const { return (wave * N + i) * LINES + (threadIdx.x & 63) / PIECES; }
     __device__ __forceinline__ int piece(int i) const {
         const int l = line(i), s = (threadIdx.x & 63) % PIECES;
-        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot<BK, GROUP>(l, s);
+        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot<BK>(l, s);
     }
     // ld, panel: elements from line to line and from panel to panel; row0: the
     // tile's first row (column) of `rows`
@@ -288,7 +287,7 @@ __device__ __forceinline__ void each(F f) {
 
 // The same tile through registers: any alignment, and fp32, cut into planes on
 // its way to LDS.
-template <class T, bool COLS, int BK, int ROWS, int GROUP, int THREADS>
+template <class T, bool COLS, int BK, int ROWS, int THREADS>
 struct RegLoad {
     static constexpr int P = Mat<T>::P, N = ROWS * BK / 8 / THREADS;
     static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;
@@ -307,7 +306,7 @@ struct RegLoad {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int id = i * THREADS + threadIdx.x, line = id / PIECES, piece = id % PIECES;
-            char* q = lds + lds_piece<COLS, BK, ROWS, GROUP>(line, piece);
+            char* q = lds + lds_piece<COLS, BK, ROWS>(line, piece);
             if constexpr (P == 1) {
                 *reinterpret_cast<Raw8<T>*>(q) = r[i];
             } else {
@@ -331,61 +330,82 @@ struct Shape {
     static constexpr int FH = KIND == FWD ? FN / 2 : FN;  // fragments of D's columns in a wave
     static constexpr int NB = KIND == FWD ? TN / 2 : TN;  // columns of D of a workgroup
     // (FWD: LDS rows [0, NB) of B are Wg's, [NB, TN) Wu's, and so are a wave's fragments)
-    // Columns of D that a lane ends up with side by side: in FWD a wave's FH fragments
-    // interleave, for stores of 16 bytes.
-    static constexpr int GROUP = KIND == FWD ? 4 * FH : 4;
-    // The row of B's tile, from the wave's first one, that is row i of fragment x.
-    static __device__ __forceinline__ int row_of(int x, int i) {
-        return KIND == FWD ? (i >> 2) * GROUP + x % FH * 4 + (i & 3) : x * 16 + i;
-    }
 };
 
+// Orders this wave's LDS writes before its later LDS reads, and those before
+// its later writes.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Results of a wave: acc[i][j][r] is D[m][n], m = i * 16 + lane % 16 and
-// n = j * 16 + lane / 16 * 4 + r. In FWD it is g for j < FH, u FH fragments on,
-// with n consecutive over (j, r) from lane / 16 * GROUP on.
-template <class T, Kind KIND, class S, int FM, int FN>
-__device__ __forceinline__ void put_out(const Product& q, const floatx4 (&acc)[FM][FN], int64_t m0, int n0) {
-    const int li = threadIdx.x & 15, lk = (threadIdx.x & 63) >> 4;
+// n = j * 16 + lane / 16 * 4 + r; in FWD the first half of the fragments j is g,
+// the second u. They pass through the wave's LDS, CI rows of fragments at a
+// time: the first half's columns through x, the second's through y (16 CI rows
+// of fp32 each). Memory then sees runs of 128 bytes and more, and the
+// activation is a short loop: unrolled over the accumulators it would be more
+// instructions than the instruction cache holds. The 16-byte pieces of a row lie
+// in the order piece ^ row.
+template <class T, Kind KIND, int CI, int FM, int FN>
+__device__ __forceinline__ void put_out(const Product& q, char* x, char* y, const floatx4 (&acc)[FM][FN], int64_t m0,
+                                        int n0) {
+    constexpr int FH = FN / 2, PIECES = FH * 4, BYTES = PIECES * 16, LANES = PIECES / 2;   // lanes of 8 columns a row
+    const int lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
     const int64_t MN = q.M * q.N;
+    float *pg = q.gate, *pu = q.up;
+    if (KIND == FWD && q.part) {
+        pg = q.part + blockIdx.y * 2 * MN;
+        pu = pg + MN;
+    }
+    float* part = q.part + (blockIdx.y * gridDim.z + blockIdx.z) * MN;
+    T* out = (T*)(blockIdx.z ? q.out2 : q.out);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        __builtin_amdgcn_sched_barrier(0);   // row by row: no registers for several at once
-        const int64_t m = m0 + i * 16 + li;
-        if (m >= q.M) continue;
-        if constexpr (KIND == FWD) {
+    for (int c = 0; c < FM; c += CI) {
+        wave_sync();
 #pragma unroll
-            for (int v = 0; v < S::GROUP; v += 8) {
-                const int n = n0 + lk * S::GROUP + v, left = q.N - n;
+        for (int i = 0; i < CI; ++i)
+#pragma unroll
+            for (int j = 0; j < FH; ++j) {
+                const int at = (i * 16 + li) * BYTES + ((j * 4 + lk) ^ (li & (PIECES - 1))) * 16;
+                *reinterpret_cast<floatx4*>(x + at) = acc[c + i][j];
+                *reinterpret_cast<floatx4*>(y + at) = acc[c + i][j + FH];
+            }
+        wave_sync();
+#pragma unroll 1
+        for (int r = lane / LANES; r < CI * 16; r += 64 / LANES) {
+            const int p = lane % LANES * 2, key = r & (PIECES - 1);
+            float a[8], b[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = r * BYTES + ((p + h) ^ key) * 16;
+                *reinterpret_cast<floatx4*>(a + h * 4) = *reinterpret_cast<const floatx4*>(x + at);
+                *reinterpret_cast<floatx4*>(b + h * 4) = *reinterpret_cast<const floatx4*>(y + at);
+            }
+            const int64_t m = m0 + c * 16 + r;
+            const int n = n0 + p * 4;
+            if (m >= q.M) continue;
+            const int64_t at = m * q.N + n;
+            if constexpr (KIND == FWD) {
+                const int left = q.N - n;
                 if (left <= 0) continue;
-                float g[8], u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    g[e] = acc[i][(v + e) / 4][e & 3];
-                    u[e] = acc[i][(v + e) / 4 + S::FH][e & 3];
-                }
-                float *pg = q.gate, *pu = q.up;
-                if (q.part) {
-                    pg = q.part + blockIdx.y * 2 * MN;
-                    pu = pg + MN;
-                } else {
+                if (!q.part) {
                     float o[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = act_of<T>(q.act, g[e]) * u[e];
+                    for (int e = 0; e < 8; ++e) o[e] = act_of<T>(q.act, a[e]) * b[e];
                     store8n((T*)q.out + m * q.ldo + n, o, left);
                 }
                 if (pg) {
-                    store8n(pg + m * q.N + n, g, left);
-                    store8n(pu + m * q.N + n, u, left);
+                    store8n(pg + at, a, left);
+                    store8n(pu + at, b, left);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int n = n0 + j * 16 + lk * 4, left = q.N - n;
-                if (left <= 0) continue;
-                const float d[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (q.part) store4n(q.part + (blockIdx.y * gridDim.z + blockIdx.z) * MN + m * q.N + n, d, left);
-                else store4n((T*)(blockIdx.z ? q.out2 : q.out) + m * q.ldo + n, d, left);
+            } else if (q.part) {
+                store8n(part + at, a, q.N - n);
+                store8n(part + at + FH * 16, b, q.N - n - FH * 16);
+            } else {
+                store8n(out + m * q.ldo + n, a, q.N - n);
+                store8n(out + m * q.ldo + n + FH * 16, b, q.N - n - FH * 16);
             }
         }
     }
@@ -412,13 +432,12 @@ __device__ __forceinline__ void mma_in_place(floatx4& c, const V& a, const V& b)
         asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
 }
 
-// Waits until the matrix instructions' results can be read: 32 cycles, tied to
-// the accumulators that are read next.
-template <int FN>
-__device__ __forceinline__ void mma_done(floatx4 (&c)[FN]) {
-#pragma unroll
-    for (int j = 0; j < FN; j += 4)
-        asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[j]), "+a"(c[j + 1]), "+a"(c[j + 2]), "+a"(c[j + 3]));
+// Waits until the last two matrix instructions' results can be read (24 cycles;
+// the earlier ones' can by then). It stands inside the loop, right behind them:
+// the compiler does not know that they are matrix instructions, and may read or
+// move accumulators anywhere after the loop.
+__device__ __forceinline__ void mma_done(floatx4& last, floatx4& before) {
+    asm volatile("s_nop 15\n\ts_nop 7" : "+a"(last), "+a"(before));
 }
 
 // 16-bit operands whose pieces are whole and aligned: tiles of 32 of the summed
@@ -443,8 +462,8 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
     const int n0 = tn * S::NB;
     const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
 
-    DmaLoad<S::AC, BK, S::TM, 4, WAVES> la;
-    DmaLoad<S::BC, BK, S::NB, S::GROUP, WAVES> lb;
+    DmaLoad<S::AC, BK, S::TM, WAVES> la;
+    DmaLoad<S::BC, BK, S::NB, WAVES> lb;
     la.init(q.lda, q.pa, m0, q.M);
     lb.init(q.ldb, q.pb, n0, q.N);
     constexpr int LOADS = la.N + lb.N * (KIND == FWD ? 2 : 1);   // a wave's a step
@@ -492,12 +511,11 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
     V f0[FN + FM], f1[FN + FM];
     auto read = [&](V (&f)[FN + FM], const char* sa, const char* sb, int x) TT_INLINE {
         if (x < FN) {
-            const int w = wn * S::FH * 16;
-            f[x] = fragment<V, S::BC, BK, S::NB, S::GROUP>(sb + x / S::FH * S::NB * BK * 2, w + S::row_of(x, li),
-                                                           w + x * 16, 0);
+            const int w = (wn * S::FH + x % S::FH) * 16;
+            f[x] = fragment<V, S::BC, BK, S::NB>(sb + x / S::FH * S::NB * BK * 2, w + li, w, 0);
         } else {
             const int r = wm * FM * 16 + (x - FN) * 16;
-            f[x] = fragment<V, S::AC, BK, S::TM, 4>(sa, r + li, r, 0);
+            f[x] = fragment<V, S::AC, BK, S::TM>(sa, r + li, r, 0);
         }
     };
     // Step s: products of its fragments f; fragments g of step s + 1 from (ta, tb), early enough
@@ -535,12 +553,14 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
             step(s + 1, f1, f0, sa1, sb1, sa2, sb2);
             step(s + 2, f0, f1, sa2, sb2, sa3, sb3);
             step(s + 3, f1, f0, sa3, sb3, sa0, sb0);
+            mma_done(acc[FM - 1][FN - 1], acc[FM - 1][FN - 2]);
         }
-        __builtin_amdgcn_s_waitcnt(0x0f70);   // no load to LDS outlives the workgroup
     }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) mma_done(acc[i]);
-    put_out<T, KIND, S>(q, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
+    landed_barrier<0>();   // no load to LDS is under way when the results pass through it
+    static_assert(WAVES == 4 && FM / (FM > 4 ? 2 : 1) * 16 * (FN / 2) * 16 * 4 <= S::TM * BK * 2, "room for a wave's results");
+    char* x = wave < 2 ? (wave == 0 ? sa0 : sa1) : (wave == 2 ? sa2 : sa3);
+    char* y = wave < 2 ? (wave == 0 ? sb0 : sb1) : (wave == 2 ? sb2 : sb3);
+    put_out<T, KIND, FM / (FM > 4 ? 2 : 1)>(q, x, y, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
 }
 
 // Operands of any type and alignment: tiles pass through registers, loaded
@@ -562,8 +582,8 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
     const int n0 = tn * S::NB;
     const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
 
-    RegLoad<T, S::AC, BK, S::TM, 4, 256> la;
-    RegLoad<T, S::BC, BK, S::NB, S::GROUP, 256> lb, lb2;
+    RegLoad<T, S::AC, BK, S::TM, 256> la;
+    RegLoad<T, S::BC, BK, S::NB, 256> lb, lb2;
     const T* pa = (const T*)q.a + (KIND == DW ? (int64_t)blockIdx.z * q.a2 : 0);
     const int half = KIND == DX ? q.steps / 2 : q.steps;
     auto load = [&](int step) {
@@ -596,16 +616,15 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     const int r = wm * FM * 16 + i * 16;
-                    fa[p][i] = fragment<V, S::AC, BK, S::TM, 4>(sa + p * PA, r + li, r, h);
+                    fa[p][i] = fragment<V, S::AC, BK, S::TM>(sa + p * PA, r + li, r, h);
                 }
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 V fb[P];
-                const int w = wn * S::FH * 16;
+                const int w = (wn * S::FH + j % S::FH) * 16;
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    fb[p] = fragment<V, S::BC, BK, S::NB, S::GROUP>(sb + (j / S::FH * P + p) * PB,
-                                                                    w + S::row_of(j, li), w + j * 16, h);
+                    fb[p] = fragment<V, S::BC, BK, S::NB>(sb + (j / S::FH * P + p) * PB, w + li, w, h);
                 if constexpr (P == 1) {
 #pragma unroll
                     for (int i = 0; i < FM; ++i) acc[i][j] = Frag<E>::mma(fb[0], fa[0][i], acc[i][j]);
@@ -619,7 +638,8 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
             }
         }
     }
-    put_out<T, KIND, S>(q, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
+    __syncthreads();
+    put_out<T, KIND, 1>(q, sa + wave * 4096, sa + wave * 4096 + 2048, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
 }
 
 // The splits' partial sums, joined in their order. FWD: both projections of
@@ -910,7 +930,7 @@ tt_status gate_backward(const GateArgs& a, const GateSpace& sp) {
     q.a2 = a.M * sp.Hp;
     q.bytes_a = a.M * 2 * sp.Hp * (int64_t)sizeof(T);
     if (a.M > 0) {
-        TT_LAUNCH(nullptr, "k_gate_grad", a.s, (k_gate_grad<T>), dim3(grid_for(a.M * (sp.Hp / 8), 256)), dim3(256), 0,
+        TT_LAUNCH(nullptr, "k_gate_grad", a.s, (k_gate_grad<T>), dim3((unsigned)((a.M + 15) / 16 * ((sp.Hp / kPanel + 3) / 4))), dim3(256), 0,
                   a.s, a.gate, a.up, (const T*)a.dout, a.lddout, a.M, (int)a.H, (int)sp.Hp, panel, a.act, gu);
         TT_LAUNCH_CHECK();
         q.b = a.wg; q.b2 = a.wu; q.ldb = a.K;
