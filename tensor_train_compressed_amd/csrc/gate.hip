@@ -46,18 +46,18 @@ struct Frag<f16> {
     }
 };
 
-// What a tensor of type T is on the matrix cores: elements E in P planes, taken
-// BK at a time.
+// What a tensor of type T is on the matrix cores: elements E in P planes.
 template <class T>
 struct Mat {
     typedef T E;
-    static constexpr int P = 1, BK = 64;
+    static constexpr int P = 1;
 };
 template <>
 struct Mat<float> {
     typedef bf16 E;
-    static constexpr int P = 3, BK = 32;
+    static constexpr int P = 3;
 };
+constexpr int kBK = 32;   // of the summed length, a step
 
 // The planes of eight values.
 template <int P>
@@ -148,6 +148,25 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
     store8n(p + M * Hp, du, 8);
 }
 
+// 16-bit operands whose rows do not start at whole 16-byte pieces, copied to rows
+// that do: dst [rows][ldd], ldd = cols up to a multiple of 8, zeros past cols.
+// Up to three operands in one launch (blockIdx.y).
+struct Align {
+    const void* src[3];
+    void* dst[3];
+    int64_t ld[3], rows[3];
+    int cols, ldd;
+};
+template <class T>
+__global__ __launch_bounds__(256) void k_gate_align(const Align a) {
+    const int z = blockIdx.y, per = a.ldd / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    if (r >= a.rows[z]) return;
+    const Raw8<T> v = load8n((const T*)a.src[z] + r * a.ld[z] + c, a.cols - c, (T)0.f);
+    *reinterpret_cast<Raw8<T>*>((T*)a.dst[z] + r * a.ldd + c) = v;
+}
+
 // ---------------------------------------------------------------------------
 // Tiles in LDS.
 //
@@ -160,17 +179,14 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
 // load of 16 lanes takes 32 bytes of four rows k, and four such groups are 8
 // rows apart.
 
-template <int BK>
-__device__ __forceinline__ int row_slot(int row, int piece) {
-    return piece ^ (BK == 64 ? row & 7 : (row >> 1) & 3);
-}
+__device__ __forceinline__ int row_slot(int row, int piece) { return piece ^ ((row >> 1) & 3); }
 __device__ __forceinline__ int col_key(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
 // Byte offset of 16-byte piece `piece` of line `line` (a row, or a k).
 template <bool COLS, int BK, int ROWS>
 __device__ __forceinline__ int lds_piece(int line, int piece) {
     if (COLS) return line * (ROWS * 2) + ((piece >> 1) ^ col_key(line)) * 32 + (piece & 1) * 16;
-    return line * (BK * 2) + row_slot<BK>(line, piece) * 16;
+    return line * (BK * 2) + row_slot(line, piece) * 16;
 }
 
 // The fragment of 16 rows (or columns) x 32 k, k in [32 h, 32 h + 32): lane l
@@ -205,7 +221,6 @@ struct Product {
     const void *a, *b, *b2;      // b2: the second weight (FWD, DX)
     int64_t lda, ldb;            // elements from line to line
     int64_t pa, pb;              // elements from panel to panel (kPanel elements of each line); kPanel: plain rows
-    int64_t bytes_a, bytes_b;    // of a, and of b and b2 each
     int64_t M;
     int N;
     int64_t K;                   // summed length; of each of two parts in DX
@@ -246,7 +261,7 @@ struct DmaLoad {
     __device__ __forceinline__ int line(int i) const { return (wave * N + i) * LINES + (threadIdx.x & 63) / PIECES; }
     __device__ __forceinline__ int piece(int i) const {
         const int l = line(i), s = (threadIdx.x & 63) % PIECES;
-        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot<BK>(l, s);
+        return COLS ? ((s >> 1) ^ col_key(l)) * 2 + (s & 1) : row_slot(l, s);
     }
     // ld, panel: elements from line to line and from panel to panel; row0: the
     // tile's first row (column) of `rows`
@@ -285,11 +300,11 @@ __device__ __forceinline__ void each(F f) {
     }
 }
 
-// The same tile through registers: any alignment, and fp32, cut into planes on
-// its way to LDS.
+// The same tile of an fp32 operand through registers, cut into planes on its way
+// to LDS.
 template <class T, bool COLS, int BK, int ROWS, int THREADS>
 struct RegLoad {
-    static constexpr int P = Mat<T>::P, N = ROWS * BK / 8 / THREADS;
+    static constexpr int N = ROWS * BK / 8 / THREADS;
     static constexpr int PIECES = COLS ? ROWS / 8 : BK / 8;
     Raw8<T> r[N];
     __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int64_t row0, int64_t rows, int64_t k0,
@@ -307,17 +322,13 @@ struct RegLoad {
         for (int i = 0; i < N; ++i) {
             const int id = i * THREADS + threadIdx.x, line = id / PIECES, piece = id % PIECES;
             char* q = lds + lds_piece<COLS, BK, ROWS>(line, piece);
-            if constexpr (P == 1) {
-                *reinterpret_cast<Raw8<T>*>(q) = r[i];
-            } else {
-                float f[8];
+            float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = r[i].at(e);
-                Raw8<bf16> c[3];
-                cut_planes(f, c);
+            for (int e = 0; e < 8; ++e) f[e] = r[i].at(e);
+            Raw8<bf16> c[3];
+            cut_planes(f, c);
 #pragma unroll
-                for (int s = 0; s < 3; ++s) *reinterpret_cast<Raw8<bf16>*>(q + s * ROWS * BK * 2) = c[s];
-            }
+            for (int s = 0; s < 3; ++s) *reinterpret_cast<Raw8<bf16>*>(q + s * ROWS * BK * 2) = c[s];
         }
     }
 };
@@ -450,7 +461,7 @@ template <class T, Kind KIND, int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(const Product q) {
     typedef Shape<KIND, WM, WN, FM, FN> S;
     typedef typename Frag<T>::V V;
-    constexpr int BK = 32, WAVES = WM * WN;
+    constexpr int BK = kBK, WAVES = WM * WN;
     // separate objects, so that the compiler sees which loads a read depends on
     __shared__ __align__(16) char sa0[S::TM * BK * 2], sb0[S::TN * BK * 2], sa1[S::TM * BK * 2], sb1[S::TN * BK * 2],
         sa2[S::TM * BK * 2], sb2[S::TN * BK * 2], sa3[S::TM * BK * 2], sb3[S::TN * BK * 2];
@@ -563,15 +574,15 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
     put_out<T, KIND, FM / (FM > 4 ? 2 : 1)>(q, x, y, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
 }
 
-// Operands of any type and alignment: tiles pass through registers, loaded
-// while the matrix cores work on the step before.
+// fp32 operands of any alignment: tiles pass through registers, where they are
+// cut into planes, loaded while the matrix cores work on the step before.
 template <class T, Kind KIND>
-__global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
+__global__ __launch_bounds__(256, 2) void k_gate_mm_cut(const Product q) {
     constexpr int FM = 4, FN = 4, WM = 2, WN = 2;
     typedef Shape<KIND, WM, WN, FM, FN> S;
     typedef typename Mat<T>::E E;
     typedef typename Frag<E>::V V;
-    constexpr int BK = Mat<T>::BK, P = Mat<T>::P;
+    constexpr int BK = kBK, P = Mat<T>::P;
     constexpr int PA = S::TM * BK * 2, PB = S::NB * BK * 2, NB2 = KIND == FWD ? 2 : 1;   // bytes of a plane
     __shared__ __align__(16) char sa[P * PA], sb[NB2 * P * PB];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -625,16 +636,11 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_any(const Product q) {
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     fb[p] = fragment<V, S::BC, BK, S::NB>(sb + (j / S::FH * P + p) * PB, w + li, w, h);
-                if constexpr (P == 1) {
 #pragma unroll
-                    for (int i = 0; i < FM; ++i) acc[i][j] = Frag<E>::mma(fb[0], fa[0][i], acc[i][j]);
-                } else {
+                for (int t = 0; t < 6; ++t)
 #pragma unroll
-                    for (int t = 0; t < 6; ++t)
-#pragma unroll
-                        for (int i = 0; i < FM; ++i)
-                            acc[i][j] = Frag<E>::mma(fb[kPlaneB[t]], fa[kPlaneA[t]][i], acc[i][j]);
-                }
+                    for (int i = 0; i < FM; ++i)
+                        acc[i][j] = Frag<E>::mma(fb[kPlaneB[t]], fa[kPlaneA[t]][i], acc[i][j]);
             }
         }
     }
@@ -796,16 +802,16 @@ constexpr int64_t kFew = 32;
 
 // How a product is cut: tiles of 256 x 256 when they fill the chip, else of
 // 128 x 128, whose summed length is split when they do not fill it either
-// (two workgroups a CU), four steps or more a split.
+// (two workgroups a CU), eight steps or more a split.
 struct Cut {
     bool big;
     int mt, nt, steps, split_steps, splits;
 };
 Cut cut_of(int32_t dtype, Kind kind, int64_t M, int64_t N, int64_t K) {
-    const int bk = dtype == TT_F32 ? 32 : 64, batch = kind == DW ? 2 : 1;
+    const int batch = kind == DW ? 2 : 1;
     const int64_t per = kind == FWD ? 2 : 1;   // columns of B of one of D
     Cut c{};
-    c.steps = (int)((K + bk - 1) / bk) * (kind == DX ? 2 : 1);
+    c.steps = (int)((K + kBK - 1) / kBK) * (kind == DX ? 2 : 1);
     auto tiles = [&](int64_t t) {
         c.mt = (int)((M + t - 1) / t);
         c.nt = (int)((N * per + t - 1) / t);
@@ -815,27 +821,42 @@ Cut cut_of(int32_t dtype, Kind kind, int64_t M, int64_t N, int64_t K) {
     c.splits = 1;
     if (!c.big) {
         const int64_t n = tiles(128);
-        if (n > 0 && n < 256) c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(512 + n - 1) / n, c.steps / 4, 64}));
+        if (n > 0 && n < 256) c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(512 + n - 1) / n, c.steps / 8, 64}));
     }
     c.split_steps = std::max(1, (c.steps + c.splits - 1) / c.splits);
     c.splits = std::max(1, (c.steps + c.split_steps - 1) / c.split_steps);
     return c;
 }
 
-// Where things lie in the workspace: the backward's dg and du, then partial sums.
+// Where things lie in the workspace (bytes): x and the weights with aligned
+// rows (16-bit types; used where the caller's are not), the backward's dg and
+// du, partial sums.
 struct GateSpace {
-    int64_t Hp;
+    int64_t Kp, Hp;
     Cut fwd, dx, dw;
-    size_t part, forward, backward;   // bytes
+    size_t x, wg, wu, gu, part, forward, backward;
     GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H)
-        : Hp(up_to(H, kPanel)), fwd(cut_of(dtype, FWD, M, H, K)), dx(cut_of(dtype, DX, M, K, Hp)),
+        : Kp(up_to(K, 8)), Hp(up_to(H, kPanel)), fwd(cut_of(dtype, FWD, M, H, K)), dx(cut_of(dtype, DX, M, K, H)),
           dw(cut_of(dtype, DW, H, K, M)) {
-        const size_t e = dtype == TT_F32 ? 4 : 2;
-        forward = M <= kFew || fwd.splits == 1 ? 0 : (size_t)fwd.splits * 2 * M * H * 4;
-        part = up_to((size_t)M * 2 * Hp * e, 256);
-        backward = part + std::max(dx.splits == 1 ? 0 : (size_t)dx.splits * M * K * 4,
-                                   dw.splits == 1 ? 0 : (size_t)dw.splits * 2 * H * K * 4);
+        size_t at = 0;
+        auto take = [&](size_t bytes) {
+            const size_t o = at;
+            at += up_to(bytes, 256);
+            return o;
+        };
+        const bool copies = dtype != TT_F32;
+        x = take(copies ? M * Kp * 2 : 0);
+        wg = take(copies ? H * Kp * 2 : 0);
+        wu = take(copies ? H * Kp * 2 : 0);
+        gu = at;
+        part = gu;
+        forward = at + (M <= kFew || fwd.splits == 1 ? 0 : (size_t)fwd.splits * 2 * M * H * 4);
+        take(M * 2 * Hp * (dtype == TT_F32 ? 4 : 2));
+        backward = at + std::max(dx.splits == 1 ? 0 : (size_t)dx.splits * M * K * 4,
+                                 dw.splits == 1 ? 0 : (size_t)dw.splits * 2 * H * K * 4);
+        part_back = at;
     }
+    size_t part_back;   // partial sums of the backward (`part`: the forward's)
 };
 
 struct GateArgs {
@@ -849,35 +870,21 @@ struct GateArgs {
 };
 
 template <class T, Kind KIND>
-tt_status product(Product q, const Cut& c, bool dma, char* part, hipStream_t s) {
+tt_status product(Product q, const Cut& c, char* part, hipStream_t s) {
     const int batch = KIND == DW ? 2 : 1;
     q.mt = c.mt;
     q.nt = c.nt;
     q.steps = c.steps;
     q.split_steps = c.split_steps;
     q.part = c.splits > 1 ? (float*)part : nullptr;
-    if (dma) {   // steps of 32, cut_of counts 64
-        q.steps *= 2;
-        q.split_steps *= 2;
+    const dim3 grid((unsigned)(q.mt * q.nt), (unsigned)c.splits, batch), block(256);
+    if constexpr (sizeof(T) == 4) {
+        TT_LAUNCH(nullptr, "k_gate_mm_cut", s, (k_gate_mm_cut<T, KIND>), grid, block, 0, s, q);
+    } else {
+        auto k = c.big ? k_gate_mm<T, KIND, 2, 2, 8, 8> : k_gate_mm<T, KIND, 2, 2, 4, 4>;
+        TT_LAUNCH(nullptr, "k_gate_mm", s, k, grid, block, 0, s, q);
     }
-    const bool big = c.big && dma;
-    if (c.big && !dma) {   // the tiles of the kernel for any alignment
-        q.mt = (int)((q.M + 127) / 128);
-        q.nt = (int)(((int64_t)q.N * (KIND == FWD ? 2 : 1) + 127) / 128);
-    }
-    const dim3 grid((unsigned)(q.mt * q.nt), (unsigned)c.splits, batch);
-    if constexpr (sizeof(T) == 2) {
-        if (big) {
-            TT_LAUNCH(nullptr, "k_gate_mm", s, (k_gate_mm<T, KIND, 2, 2, 8, 8>), grid, dim3(256), 0, s, q);
-        } else if (dma) {
-            TT_LAUNCH(nullptr, "k_gate_mm", s, (k_gate_mm<T, KIND, 2, 2, 4, 4>), grid, dim3(256), 0, s, q);
-        }
-        TT_LAUNCH_CHECK();
-    }
-    if (!dma) {
-        TT_LAUNCH(nullptr, "k_gate_mm_any", s, (k_gate_mm_any<T, KIND>), grid, dim3(256), 0, s, q);
-        TT_LAUNCH_CHECK();
-    }
+    TT_LAUNCH_CHECK();
     if (c.splits > 1) {
         const unsigned g = grid_for(q.M * ((q.N + 7) / 8), 256);
         if constexpr (KIND == FWD)
@@ -889,12 +896,44 @@ tt_status product(Product q, const Cut& c, bool dma, char* part, hipStream_t s) 
     return TT_OK;
 }
 
-// Whether tiles can go straight to LDS: whole, aligned pieces of 16 bytes in
-// every operand that the caller lays out (hidden may be any size).
+// x and the weights as the products take them: as they are, or (16-bit types)
+// copied to the workspace where a row does not start at a whole 16-byte piece.
+struct Inputs {
+    const void *x, *wg, *wu;
+    int64_t ldx, ldw;
+};
 template <class T>
-bool dma_ok(const GateArgs& a) {
-    const uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.wg | (uintptr_t)a.wu;
-    return sizeof(T) == 2 && a.K % 8 == 0 && a.ldx % 8 == 0 && (p & 15) == 0 && a.M <= (1 << 20);
+tt_status aligned_inputs(Inputs& in, const GateArgs& a, const GateSpace& sp) {
+    in = Inputs{a.x, a.wg, a.wu, a.ldx, a.K};
+    if (sizeof(T) == 4) return TT_OK;
+    const bool x = a.K % 8 != 0 || a.ldx % 8 != 0 || ((uintptr_t)a.x & 15) != 0;
+    const bool w = a.K % 8 != 0 || (((uintptr_t)a.wg | (uintptr_t)a.wu) & 15) != 0;
+    Align c{};
+    c.cols = (int)a.K;
+    c.ldd = (int)sp.Kp;
+    int n = 0;
+    auto take = [&](const void*& p, int64_t ld, int64_t rows, size_t at) {
+        c.src[n] = p;
+        c.ld[n] = ld;
+        c.rows[n] = rows;
+        c.dst[n++] = a.ws + at;
+        p = a.ws + at;
+    };
+    if (x && a.M > 0) {
+        take(in.x, a.ldx, a.M, sp.x);
+        in.ldx = sp.Kp;
+    }
+    if (w) {
+        take(in.wg, a.K, a.H, sp.wg);
+        take(in.wu, a.K, a.H, sp.wu);
+        in.ldw = sp.Kp;
+    }
+    if (n == 0) return TT_OK;
+    const int64_t rows = std::max(c.rows[0], c.rows[n - 1]);
+    TT_LAUNCH(nullptr, "k_gate_align", a.s, (k_gate_align<T>), dim3(grid_for(rows * (sp.Kp / 8), 256), n), dim3(256),
+              0, a.s, c);
+    TT_LAUNCH_CHECK();
+    return TT_OK;
 }
 
 template <class T>
@@ -903,8 +942,6 @@ tt_status gate_forward(const GateArgs& a, const GateSpace& sp) {
     q.a = a.x; q.b = a.wg; q.b2 = a.wu;
     q.lda = a.ldx; q.ldb = a.K;
     q.pa = q.pb = kPanel;
-    q.bytes_a = ((a.M - 1) * a.ldx + a.K) * (int64_t)sizeof(T);
-    q.bytes_b = a.H * a.K * (int64_t)sizeof(T);
     q.M = a.M; q.N = (int)a.H; q.K = a.K;
     q.out = a.out; q.ldo = a.ldout;
     q.gate = a.gate; q.up = a.up; q.act = a.act;
@@ -914,37 +951,42 @@ tt_status gate_forward(const GateArgs& a, const GateSpace& sp) {
         TT_LAUNCH_CHECK();
         return TT_OK;
     }
-    return product<T, FWD>(q, sp.fwd, dma_ok<T>(a), a.ws, a.s);
+    Inputs in;
+    const tt_status st = aligned_inputs<T>(in, a, sp);
+    if (st != TT_OK) return st;
+    q.a = in.x; q.b = in.wg; q.b2 = in.wu;
+    q.lda = in.ldx; q.ldb = in.ldw;
+    return product<T, FWD>(q, sp.fwd, a.ws + sp.part, a.s);
 }
 
 template <class T>
 tt_status gate_backward(const GateArgs& a, const GateSpace& sp) {
-    T* gu = (T*)a.ws;
+    T* gu = (T*)(a.ws + sp.gu);
+    const int panel = sizeof(T) == 2 ? kPanel : (int)sp.Hp;
+    Inputs in;
+    tt_status st = aligned_inputs<T>(in, a, sp);
+    if (st != TT_OK) return st;
     Product q{};
-    const bool dma = dma_ok<T>(a);
-    const int panel = dma ? kPanel : (int)sp.Hp;
     q.a = gu;
     q.lda = panel;
-    q.pa = dma ? a.M * kPanel : kPanel;
+    q.pa = sizeof(T) == 2 ? a.M * kPanel : kPanel;
     q.pb = kPanel;
     q.a2 = a.M * sp.Hp;
-    q.bytes_a = a.M * 2 * sp.Hp * (int64_t)sizeof(T);
     if (a.M > 0) {
-        TT_LAUNCH(nullptr, "k_gate_grad", a.s, (k_gate_grad<T>), dim3((unsigned)((a.M + 15) / 16 * ((sp.Hp / kPanel + 3) / 4))), dim3(256), 0,
-                  a.s, a.gate, a.up, (const T*)a.dout, a.lddout, a.M, (int)a.H, (int)sp.Hp, panel, a.act, gu);
+        TT_LAUNCH(nullptr, "k_gate_grad", a.s, (k_gate_grad<T>),
+                  dim3((unsigned)((a.M + 15) / 16 * ((sp.Hp / kPanel + 3) / 4))), dim3(256), 0, a.s, a.gate, a.up,
+                  (const T*)a.dout, a.lddout, a.M, (int)a.H, (int)sp.Hp, panel, a.act, gu);
         TT_LAUNCH_CHECK();
-        q.b = a.wg; q.b2 = a.wu; q.ldb = a.K;
-        q.bytes_b = a.H * a.K * (int64_t)sizeof(T);
+        q.b = in.wg; q.b2 = in.wu; q.ldb = in.ldw;
         q.M = a.M; q.N = (int)a.K; q.K = a.H;
         q.out = a.dx; q.ldo = a.lddx;
-        const tt_status st = product<T, DX>(q, sp.dx, dma, a.ws + sp.part, a.s);
+        st = product<T, DX>(q, sp.dx, a.ws + sp.part_back, a.s);
         if (st != TT_OK) return st;
     }
-    q.b = a.x; q.b2 = nullptr; q.ldb = a.ldx;
-    q.bytes_b = ((a.M - 1) * a.ldx + a.K) * (int64_t)sizeof(T);
+    q.b = in.x; q.b2 = nullptr; q.ldb = in.ldx;
     q.M = a.H; q.N = (int)a.K; q.K = a.M;
     q.out = a.dwg; q.out2 = a.dwu; q.ldo = a.K;
-    return product<T, DW>(q, sp.dw, dma, a.ws + sp.part, a.s);
+    return product<T, DW>(q, sp.dw, a.ws + sp.part_back, a.s);
 }
 
 tt_status gate_by_type(int32_t dtype, const GateArgs& a, bool backward) {

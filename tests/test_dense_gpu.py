@@ -417,7 +417,8 @@ def operators_once(seed):
     loss, dz = torch.empty(20, device=DEV), torch.empty_like(z)
     loss2, dz2, stats = torch.empty(20, device=DEV), torch.empty_like(z), torch.empty(20, 2, device=DEV)
     ws = [torch.empty(tte.tt_emb_norm_workspace_bytes(BF16, 300, 256), dtype=torch.uint8, device=DEV),
-          torch.empty(tte.tt_emb_gate_workspace_bytes(F32, 200, 192, 320), dtype=torch.uint8, device=DEV),
+          torch.empty(max(tte.tt_emb_gate_workspace_bytes(t, 200, 192, 320) for t in (BF16, F32)), dtype=torch.uint8,
+                      device=DEV),
           torch.empty(tte.tt_emb_distill_workspace_bytes(F16, 20, 40000), dtype=torch.uint8, device=DEV)]
 
     def call(stream=None):
