@@ -113,6 +113,22 @@ def test_distill_refusals():
     assert lib.tt_emb_distill_workspace_bytes(0, 2, 0) == 0
 
 
+def test_benchmark_counters_outlive_the_dense_sources(tmp_path, monkeypatch):
+    """The benchmark's recorded HBM counters belong to the embedding's sources alone."""
+    import shutil
+
+    import bench
+    assert bench.kernel_source_hash()
+    shutil.copytree(bench.CSRC, tmp_path / "csrc")
+    monkeypatch.setattr(bench, "CSRC", str(tmp_path / "csrc"))
+    first = bench.kernel_source_hash()
+    for f in ("gate.hip", "norm.hip", "distill.hip", "tt_dense.h"):
+        (tmp_path / "csrc" / f).write_text("changed")
+        assert bench.kernel_source_hash() == first, f
+    (tmp_path / "csrc" / "plan.hip").write_text("changed")
+    assert bench.kernel_source_hash() != first
+
+
 def test_binding_refuses_what_the_abi_cannot_see():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError, match="device tensor"):
