@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 from typing import Optional, Sequence
 
@@ -105,6 +106,8 @@ class _View(ctypes.Structure):
 def load_library() -> ctypes.CDLL:
     """Load libtt_emb.so from the package directory (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -201,6 +204,16 @@ def make_tables(tables: Sequence, g_offsets) -> ctypes.Array:
     return arr
 
 
+_names = {}   # of the dtypes seen: making a dtype's name takes 0.4 us
+
+
+def _name(dtype) -> str:
+    name = _names.get(dtype)
+    if name is None:
+        name = _names[dtype] = str(dtype).replace("torch.", "")
+    return name
+
+
 def _dev_ptr(t, dtype_name: str, what: str, numel: Optional[int] = None,
              at_least: bool = False) -> Optional[int]:
     """data_ptr() of a contiguous device tensor of the given dtype; with
@@ -210,12 +223,13 @@ def _dev_ptr(t, dtype_name: str, what: str, numel: Optional[int] = None,
         return None
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
-    if str(t.dtype) != f"torch.{dtype_name}":
-        raise ValueError(f"{what} must be {dtype_name}, got {t.dtype}")
+    dt = t.dtype
+    if (_names.get(dt) or _name(dt)) != dtype_name:
+        raise ValueError(f"{what} must be {dtype_name}, got {dt}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     if numel is not None:
-        n = int(t.numel())
+        n = t.numel()
         if (n < numel) if at_least else (n != numel):
             raise ValueError(f"{what} has {n} elements, needs {'at least ' if at_least else ''}{numel}")
     return t.data_ptr()
@@ -236,9 +250,9 @@ def core_extents(tables_c) -> tuple:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         # the handle of torch.cuda.current_stream(), without making a Stream object (2.8 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        c = sys.modules["torch"]._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -509,19 +523,15 @@ def plan_table(plan: Plan, name: str, n: int):
 # ---------------------------------------------------------------------------
 # Dense operators: layer norm, the gated feed-forward block, distillation.
 
-_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1, "torch.float16": 2}
+_DTYPES = {"float32": 0, "bfloat16": 1, "float16": 2}
 _ACTS = {"silu": 0, "gelu": 1, "relu": 2}
 
 
 def _dtype_code(dtype, what: str) -> int:
-    code = _DTYPES.get(str(dtype))
+    code = _DTYPES.get(_names.get(dtype) or _name(dtype))
     if code is None:
         raise ValueError(f"{what} must be float32, bfloat16 or float16, got {dtype}")
     return code
-
-
-def _name(dtype) -> str:
-    return str(dtype).replace("torch.", "")
 
 
 def _matrix(t, dtype, what: str, rows: Optional[int] = None, cols: Optional[int] = None):
@@ -530,13 +540,15 @@ def _matrix(t, dtype, what: str, rows: Optional[int] = None, cols: Optional[int]
         raise ValueError(f"{what} must be a device tensor")
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {_name(dtype)}, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         want = f"[{'rows' if rows is None else rows}, {'cols' if cols is None else cols}]"
-        raise ValueError(f"{what} must be {want}, got {list(t.shape)}")
-    r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must be {want}, got {list(shape)}")
+    r, c = shape
+    stride = t.stride()
+    if c > 1 and stride[1] != 1:
         raise ValueError(f"{what} must have contiguous columns")
-    ld = int(t.stride(0)) if r > 1 else c
+    ld = stride[0] if r > 1 else c
     if ld < c:
         raise ValueError(f"{what}'s rows overlap (row stride {ld}, {c} columns)")
     return t.data_ptr(), ld
@@ -549,13 +561,15 @@ def _pair(a, b, what: str):
     return a is not None
 
 
-def _workspace(workspace, need: int, what: str, device, stream):
-    """(tensor, data_ptr, bytes) of the caller's workspace, or of one allocated
-    here with torch on the stream that uses it."""
-    if need == 0:
-        raise TTEmbError(TT_ERR_UNSUPPORTED, what)
+def _workspace(workspace, bytes_call, sizes, what: str, like, stream):
+    """(tensor, data_ptr, bytes) of the caller's workspace, whose size the call
+    itself checks, or of one allocated here with torch on the stream that uses it."""
     if workspace is None:
+        need = bytes_call(*sizes)
+        if need == 0:
+            raise TTEmbError(TT_ERR_UNSUPPORTED, what)
         import torch
+        device = like.device
         s = stream
         if s is None:
             s = torch.cuda.current_stream(device)
@@ -593,8 +607,8 @@ def tt_emb_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias=None, wor
     pdy, lddy = _matrix(dy, x.dtype, "dy", rows, dim)
     pdx, lddx = _matrix(dx, x.dtype, "dx", rows, dim)
     wname = _name(weight.dtype)
-    ws, pws, nws = _workspace(workspace, tt_emb_norm_workspace_bytes(x.dtype, rows, dim), "tt_emb_norm_backward",
-                              x.device, stream)
+    ws, pws, nws = _workspace(workspace, tt_emb_norm_workspace_bytes, (x.dtype, rows, dim), "tt_emb_norm_backward",
+                              x, stream)
     _check(load_library().tt_emb_norm_backward(
         code, wcode, px, ldx, _dev_ptr(weight, wname, "weight", dim), _dev_ptr(mean, "float32", "mean", rows),
         _dev_ptr(rstd, "float32", "rstd", rows), pdy, lddy, pdx, lddx, _dev_ptr(dweight, wname, "dweight", dim),
@@ -625,8 +639,8 @@ def tt_emb_gate_forward(x, w_gate, w_up, out, gate=None, up=None, act: str = "si
     code, px, ldx, pg, pu, rows, dim, hidden = _gate_sizes(x, w_gate, w_up, act)
     po, ldo = _matrix(out, x.dtype, "out", rows, hidden)
     _pair(gate, up, "gate and up")
-    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes(x.dtype, rows, dim, hidden),
-                              "tt_emb_gate_forward", x.device, stream)
+    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes, (x.dtype, rows, dim, hidden),
+                              "tt_emb_gate_forward", x, stream)
     _check(load_library().tt_emb_gate_forward(
         code, px, ldx, pg, pu, po, ldo, _dev_ptr(gate, "float32", "gate", rows * hidden),
         _dev_ptr(up, "float32", "up", rows * hidden), rows, dim, hidden, _ACTS[act], pws, nws, _stream(stream)),
@@ -640,8 +654,8 @@ def tt_emb_gate_backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, ac
     pd, ldd = _matrix(dout, x.dtype, "dout", rows, hidden)
     pdx, lddx = _matrix(dx, x.dtype, "dx", rows, dim)
     name = _name(x.dtype)
-    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes(x.dtype, rows, dim, hidden),
-                              "tt_emb_gate_backward", x.device, stream)
+    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes, (x.dtype, rows, dim, hidden),
+                              "tt_emb_gate_backward", x, stream)
     _check(load_library().tt_emb_gate_backward(
         code, px, ldx, pg, pu, _dev_ptr(gate, "float32", "gate", rows * hidden),
         _dev_ptr(up, "float32", "up", rows * hidden), pd, ldd, pdx, lddx,
@@ -670,8 +684,8 @@ def tt_emb_distill_forward(logits, ids, top_logits, loss, stats=None, temperatur
     """Each row's loss against the teacher's list; stats (float32 [rows, 2])
     is kept for tt_emb_distill_backward when given."""
     code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
-    ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes(logits.dtype, rows, classes),
-                              "tt_emb_distill_forward", logits.device, stream)
+    ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes, (logits.dtype, rows, classes),
+                              "tt_emb_distill_forward", logits, stream)
     _check(load_library().tt_emb_distill_forward(
         code, pz, ld, pi, pt, top, _dev_ptr(loss, "float32", "loss", rows),
         _dev_ptr(stats, "float32", "stats", rows * 2), rows, classes, float(temperature), pws, nws,
@@ -695,8 +709,8 @@ def tt_emb_distill_train(logits, ids, top_logits, row_weight, loss, dlogits, tem
     """tt_emb_distill_forward and tt_emb_distill_backward in one call."""
     code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
     pd, ldd = _matrix(dlogits, logits.dtype, "dlogits", rows, classes)
-    ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes(logits.dtype, rows, classes),
-                              "tt_emb_distill_train", logits.device, stream)
+    ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes, (logits.dtype, rows, classes),
+                              "tt_emb_distill_train", logits, stream)
     _check(load_library().tt_emb_distill_train(
         code, pz, ld, pi, pt, top, _dev_ptr(row_weight, "float32", "row_weight", rows),
         _dev_ptr(loss, "float32", "loss", rows), pd, ldd, rows, classes, float(temperature), pws, nws,
