@@ -110,6 +110,20 @@ def test_norm_offset_and_constant_rows():
     check_norm(x, rand(300, seed=2), rand(300, seed=3), rand(6, 300, seed=4))
 
 
+def test_norm_far_rows():
+    """Rows far from zero beside their spread: the statistics are good to the rounding of the inputs' own sums."""
+    x = (rand(40, 3000, seed=1) + 3e4 * rand(40, 1, seed=2)).to(F32)
+    y, mean, rstd = torch.empty_like(x), torch.empty(40, device=DEV), torch.empty(40, device=DEV)
+    w, b = torch.ones(3000, device=DEV), torch.zeros(3000, device=DEV)
+    tte.tt_emb_norm_forward(x, w, b, y, mean, rstd)
+    wy, wm, wr, _ = ref.norm(x, w, b, 1e-5)
+    # x - mean: the first mean is off by a few roundings of it, the second sum takes that off again,
+    # each difference is off by half a step of itself
+    assert float((mean.double() - wm[:, 0]).abs().max() / wm.abs().max()) <= 2 * ref.U32
+    assert float((rstd.double() / wr[:, 0] - 1).abs().max()) <= ref.LEVELS * ref.U32
+    assert float((y.double() - wy).abs().max()) <= ref.LEVELS * ref.U32 * float(wy.abs().max())
+
+
 def test_norm_bad_rows_stay_apart():
     """A row with NaN or an infinity makes that row NaN and no other."""
     x, w, b, dy = rand(5, 200, seed=1), rand(200, seed=2), rand(200, seed=3), rand(5, 200, seed=4)
