@@ -331,6 +331,14 @@ def test_distill_sizes(dt, m, v, top, pad, off):
     check_distill((2 * rand(m, v, seed=1)).to(dt), ids, tl, w, t, pad, off)
 
 
+def test_distill_more_rows_than_one_launch_takes():
+    """2^23 workgroups go in one launch."""
+    m = (1 << 23) + 1001
+    z = rand(m, 2, seed=1, dt=F16)
+    ids = torch.randint(-1, 3, (m, 1), generator=torch.Generator(device=DEV).manual_seed(2), device=DEV)
+    check_distill(z, ids, rand(m, 1, seed=3), rand(m, seed=4), 2.0)
+
+
 def test_distill_no_list():
     z = rand(3, 100, seed=1)
     ids, tl, w = teacher(3, 100, 0, seed=1)
