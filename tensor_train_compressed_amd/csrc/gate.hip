@@ -65,20 +65,17 @@ struct Planes {
     Raw8<bf16> p[P];
 };
 __device__ __forceinline__ void cut_planes(const float (&f)[8], Raw8<bf16> (&out)[3]) {
-    float x0[8], x1[8], x2[8];
+    // values that 8 digits would round up to infinity start from the largest finite one
+    constexpr float kTop = 3.38953139e38f;   // 0xFF 2^120
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        // values that 8 digits would round up to infinity start from the largest finite one
-        constexpr float kTop = 3.38953139e38f;   // 0xFF 2^120
-        const float x = f[e];
-        x0[e] = (float)(bf16)__builtin_amdgcn_fmed3f(x, -kTop, kTop);
-        const float r = x - x0[e];
-        x1[e] = (float)(bf16)r;
-        x2[e] = r - x1[e];
+    for (int i = 0; i < 4; ++i) {
+        float a = f[2 * i], b = f[2 * i + 1];
+        out[0].w[i] = word_of<bf16>(__builtin_amdgcn_fmed3f(a, -kTop, kTop), __builtin_amdgcn_fmed3f(b, -kTop, kTop));
+        a -= out[0].at(2 * i);
+        b -= out[0].at(2 * i + 1);
+        out[1].w[i] = word_of<bf16>(a, b);
+        out[2].w[i] = word_of<bf16>(a - out[1].at(2 * i), b - out[1].at(2 * i + 1));
     }
-    out[0].set(x0);
-    out[1].set(x1);
-    out[2].set(x2);
 }
 // The six plane products, the smallest first.
 __device__ constexpr int kPlaneA[6] = {2, 0, 1, 1, 0, 0}, kPlaneB[6] = {0, 2, 1, 0, 1, 0};

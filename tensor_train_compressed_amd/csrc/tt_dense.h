@@ -24,6 +24,15 @@ __device__ __forceinline__ uint32_t bits_of(T v) {
     else return __builtin_bit_cast(uint16_t, v);
 }
 
+// Two values rounded to the nearest T, in one word (bf16: one instruction; rounded
+// one by one they would take two and a third to join them).
+template <class T>
+__device__ __forceinline__ uint32_t word_of(float a, float b) {
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    typedef T Tx2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), Tx2));
+}
+
 // Eight consecutive elements as they sit in memory, kept as 32-bit words (an
 // array of 16-bit elements would take a register each). Rows of any width and
 // stride are served by one code path: the copies below take the element's own
@@ -48,7 +57,7 @@ struct alignas(16) Raw8 {
 #pragma unroll
         for (int i = 0; i < (int)(2 * sizeof(T)); ++i) {
             if constexpr (sizeof(T) == 4) w[i] = bits_of(f[i]);
-            else w[i] = bits_of((T)f[2 * i]) | bits_of((T)f[2 * i + 1]) << 16;
+            else w[i] = word_of<T>(f[2 * i], f[2 * i + 1]);
         }
     }
 };
