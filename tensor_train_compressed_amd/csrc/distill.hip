@@ -90,16 +90,6 @@ __device__ __forceinline__ void chunk_load(Raw8<T> (&r)[kVecs], const T* __restr
     }
 }
 
-// Keeps the raw words as what later passes unpack again: the compiler would
-// otherwise hold a chunk's floats, twice the registers, from one pass to the next.
-template <class T>
-__device__ __forceinline__ void keep_raw(Raw8<T> (&r)[kVecs]) {
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-        for (int i = 0; i < (int)(2 * sizeof(T)); ++i) asm volatile("" : "+v"(r[v].w[i]));
-}
-
 template <class T>
 __device__ __forceinline__ MaxSum chunk_stats(Raw8<T> (&r)[kVecs], int n, float c, float* sm) {
     float m = -INFINITY;

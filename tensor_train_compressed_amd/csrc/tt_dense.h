@@ -85,6 +85,16 @@ __device__ __forceinline__ Raw8<T> load8n(const T* __restrict__ p, int n, T fill
     return r;
 }
 
+// Keeps the raw words as what later passes unpack again: the compiler would
+// otherwise hold the floats, twice the registers, from one pass to the next.
+template <class T, int N>
+__device__ __forceinline__ void keep_raw(Raw8<T> (&r)[N]) {
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+#pragma unroll
+        for (int i = 0; i < (int)(2 * sizeof(T)); ++i) asm volatile("" : "+v"(r[v].w[i]));
+}
+
 template <class T>
 __device__ __forceinline__ void store8n(T* __restrict__ p, const float (&f)[8], int n) {
     if (n >= 8) {
