@@ -251,16 +251,25 @@ struct Product {
     int act;
     float* part;                 // partial sums, when the summed length is split: [split][FWD: 2, DW: 2][M][N]
     int steps, split_steps;      // BK-steps in all, and of a split
-    int mt, nt;                  // tiles
+    int mt, nt, splits;          // tiles
 };
 
-// Tile of a workgroup: workgroups run on XCD blockIdx mod 8, so each XCD takes
+// A workgroup's part of a product: tile, split, and which of DW's two results.
+struct Place {
+    int tile, split, z;
+};
+__device__ __forceinline__ Place place_of(const Product& q, int block) {
+    const int tiles = q.mt * q.nt, rest = block / tiles;
+    return {block - rest * tiles, rest % q.splits, rest / q.splits};
+}
+
+// Tile of a workgroup: workgroups run on XCD index mod 8, so each XCD takes
 // a run of consecutive tiles, and a run goes down bands of 8 rows of tiles,
 // whose operands its L2 then holds.
-__device__ __forceinline__ void tile_of(const Product& q, int& tm, int& tn) {
+__device__ __forceinline__ void tile_of(const Product& q, int index, int& tm, int& tn) {
     const int all = q.mt * q.nt, per = all / kXcds, rest = all % kXcds;
-    const int x = blockIdx.x % kXcds;
-    const int t = x * per + min(x, rest) + blockIdx.x / kXcds;
+    const int x = index % kXcds;
+    const int t = x * per + min(x, rest) + index / kXcds;
     const int band = t / (8 * q.nt), rows = min(8, q.mt - band * 8), in = t - band * 8 * q.nt;
     tm = band * 8 + in % rows;
     tn = in / rows;
@@ -380,18 +389,18 @@ __device__ __forceinline__ void wave_sync() {
 // instructions than the instruction cache holds. The 16-byte pieces of a row lie
 // in the order piece ^ row.
 template <class T, Kind KIND, int CI, int FM, int FN>
-__device__ __forceinline__ void put_out(const Product& q, char* x, char* y, const floatx4 (&acc)[FM][FN], int64_t m0,
-                                        int n0) {
+__device__ __forceinline__ void put_out(const Product& q, Place place, char* x, char* y, const floatx4 (&acc)[FM][FN],
+                                        int64_t m0, int n0) {
     constexpr int FH = FN / 2, PIECES = FH * 4, BYTES = PIECES * 16, LANES = PIECES / 2;   // lanes of 8 columns a row
     const int lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
     const int64_t MN = q.M * q.N;
     float *pg = q.gate, *pu = q.up;
     if (KIND == FWD && q.part) {
-        pg = q.part + blockIdx.y * 2 * MN;
+        pg = q.part + place.split * 2 * MN;
         pu = pg + MN;
     }
-    float* part = q.part + (blockIdx.y * gridDim.z + blockIdx.z) * MN;
-    T* out = (T*)(blockIdx.z ? q.out2 : q.out);
+    float* part = q.part + (place.split * (KIND == DW ? 2 : 1) + place.z) * MN;
+    T* out = (T*)(place.z ? q.out2 : q.out);
 #pragma unroll
     for (int c = 0; c < FM; c += CI) {
         wave_sync();
@@ -477,21 +486,22 @@ __device__ __forceinline__ void mma_done(floatx4& last, floatx4& before) {
 // step's fragments are read and the loads of the one four steps on are issued,
 // both spread over the products: three steps are under way all the time, which
 // covers the latency of the caches past L2. One barrier a step.
+//
+// The ring's tiles are separate objects, so that the compiler sees which loads a
+// read depends on.
 template <class T, Kind KIND, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(const Product q) {
+__device__ __forceinline__ void mm(const Product& q, const Place place, char* sa0, char* sb0, char* sa1, char* sb1,
+                                   char* sa2, char* sb2, char* sa3, char* sb3) {
     typedef Shape<KIND, WM, WN, FM, FN> S;
     typedef typename Frag<T>::V V;
     constexpr int BK = kBK, WAVES = WM * WN;
-    // separate objects, so that the compiler sees which loads a read depends on
-    __shared__ __align__(16) char sa0[S::TM * BK * 2], sb0[S::TN * BK * 2], sa1[S::TM * BK * 2], sb1[S::TN * BK * 2],
-        sa2[S::TM * BK * 2], sb2[S::TN * BK * 2], sa3[S::TM * BK * 2], sb3[S::TN * BK * 2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN, li = lane & 15;
     int tm, tn;
-    tile_of(q, tm, tn);
+    tile_of(q, place.tile, tm, tn);
     const int64_t m0 = (int64_t)tm * S::TM;
     const int n0 = tn * S::NB;
-    const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
+    const int s0 = place.split * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
 
     DmaLoad<S::AC, BK, S::TM, WAVES> la;
     DmaLoad<S::BC, BK, S::NB, WAVES> lb;
@@ -499,7 +509,7 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
     lb.init(q.ldb, q.pb, n0, q.N);
     constexpr int LOADS = la.N + lb.N * (KIND == FWD ? 2 : 1);   // a wave's a step
     static_assert(BK == kPanel && S::TM % kPanel == 0 && S::NB % kPanel == 0, "tiles are whole panels");
-    const int64_t ta = (S::AC ? m0 / kPanel * q.pa : m0 * q.lda) * 2 + (KIND == DW ? (int64_t)blockIdx.z * q.a2 * 2 : 0);
+    const int64_t ta = (S::AC ? m0 / kPanel * q.pa : m0 * q.lda) * 2 + (KIND == DW ? (int64_t)place.z * q.a2 * 2 : 0);
     const int64_t tb = (S::BC ? n0 / kPanel * q.pb : n0 * q.ldb) * 2;
     const int64_t da = (S::AC ? BK * q.lda : q.pa) * 2, db = (S::BC ? BK * q.ldb : q.pb) * 2;   // from step to step
     // DX: the steps of dg and Wg, then those of du and Wu
@@ -591,31 +601,53 @@ __global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(
     static_assert(WAVES == 4 && FM / (FM > 4 ? 2 : 1) * 16 * (FN / 2) * 16 * 4 <= S::TM * BK * 2, "room for a wave's results");
     char* x = wave < 2 ? (wave == 0 ? sa0 : sa1) : (wave == 2 ? sa2 : sa3);
     char* y = wave < 2 ? (wave == 0 ? sb0 : sb1) : (wave == 2 ? sb2 : sb3);
-    put_out<T, KIND, FM / (FM > 4 ? 2 : 1)>(q, x, y, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
+    put_out<T, KIND, FM / (FM > 4 ? 2 : 1)>(q, place, x, y, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
 }
+
+#define TT_RING(SIZE_A, SIZE_B)                                                                                    \
+    __shared__ __align__(16) char sa0[SIZE_A], sb0[SIZE_B], sa1[SIZE_A], sb1[SIZE_B], sa2[SIZE_A], sb2[SIZE_B],    \
+        sa3[SIZE_A], sb3[SIZE_B]
+
+template <class T, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm(const Product q) {
+    TT_RING(WM * FM * 16 * kBK * 2, WN * FN * 16 * kBK * 2);
+    mm<T, FWD, WM, WN, FM, FN>(q, place_of(q, blockIdx.x), sa0, sb0, sa1, sb1, sa2, sb2, sa3, sb3);
+}
+
+// The backward's products in one launch, dx's workgroups first: neither waits for
+// the other, and their last workgroups fill the chip together.
+template <class T, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM* WN * 64, FM * FN <= 32 ? 2 : 1) void k_gate_mm_back(const Product dx, const Product dw) {
+    TT_RING(WM * FM * 16 * kBK * 2, WN * FN * 16 * kBK * 2);
+    const int n = dx.mt * dx.nt * dx.splits, b = blockIdx.x;
+    if (b < n) mm<T, DX, WM, WN, FM, FN>(dx, place_of(dx, b), sa0, sb0, sa1, sb1, sa2, sb2, sa3, sb3);
+    else mm<T, DW, WM, WN, FM, FN>(dw, place_of(dw, b - n), sa0, sb0, sa1, sb1, sa2, sb2, sa3, sb3);
+}
+
+constexpr int kCutBytes = 3 * 128 * kBK * 2;   // of 128 rows' planes
 
 // fp32 operands of any alignment: tiles pass through registers, where they are
 // cut into planes, loaded while the matrix cores work on the step before.
 template <class T, Kind KIND>
-__global__ __launch_bounds__(256, 2) void k_gate_mm_cut(const Product q) {
+__device__ __forceinline__ void mm_cut(const Product& q, const Place place, char* sa, char* sb) {
     constexpr int FM = 4, FN = 4, WM = 2, WN = 2;
     typedef Shape<KIND, WM, WN, FM, FN> S;
     typedef typename Mat<T>::E E;
     typedef typename Frag<E>::V V;
     constexpr int BK = kBK, P = Mat<T>::P;
-    constexpr int PA = S::TM * BK * 2, PB = S::NB * BK * 2, NB2 = KIND == FWD ? 2 : 1;   // bytes of a plane
-    __shared__ __align__(16) char sa[P * PA], sb[NB2 * P * PB];
+    constexpr int PA = S::TM * BK * 2, PB = S::NB * BK * 2;   // bytes of a plane
+    static_assert(P * PA <= kCutBytes && (KIND == FWD ? 2 : 1) * P * PB <= kCutBytes, "room for the planes");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN, li = lane & 15;
     int tm, tn;
-    tile_of(q, tm, tn);
+    tile_of(q, place.tile, tm, tn);
     const int64_t m0 = (int64_t)tm * S::TM;
     const int n0 = tn * S::NB;
-    const int s0 = blockIdx.y * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
+    const int s0 = place.split * q.split_steps, s1 = min(q.steps, s0 + q.split_steps);
 
     RegLoad<T, S::AC, BK, S::TM, 256> la;
     RegLoad<T, S::BC, BK, S::NB, 256> lb, lb2;
-    const T* pa = (const T*)q.a + (KIND == DW ? (int64_t)blockIdx.z * q.a2 : 0);
+    const T* pa = (const T*)q.a + (KIND == DW ? (int64_t)place.z * q.a2 : 0);
     const int half = KIND == DX ? q.steps / 2 : q.steps;
     auto load = [&](int step) {
         const bool second = KIND == DX && step >= half;
@@ -665,13 +697,27 @@ __global__ __launch_bounds__(256, 2) void k_gate_mm_cut(const Product q) {
         }
     }
     __syncthreads();
-    put_out<T, KIND, 1>(q, sa + wave * 4096, sa + wave * 4096 + 2048, acc, m0 + wm * FM * 16, n0 + wn * S::FH * 16);
+    put_out<T, KIND, 1>(q, place, sa + wave * 4096, sa + wave * 4096 + 2048, acc, m0 + wm * FM * 16,
+                        n0 + wn * S::FH * 16);
+}
+
+template <class T>
+__global__ __launch_bounds__(256, 2) void k_gate_mm_cut(const Product q) {
+    __shared__ __align__(16) char sa[kCutBytes], sb[kCutBytes];
+    mm_cut<T, FWD>(q, place_of(q, blockIdx.x), sa, sb);
+}
+template <class T>
+__global__ __launch_bounds__(256, 2) void k_gate_mm_cut_back(const Product dx, const Product dw) {
+    __shared__ __align__(16) char sa[kCutBytes], sb[kCutBytes];
+    const int n = dx.mt * dx.nt * dx.splits, b = blockIdx.x;
+    if (b < n) mm_cut<T, DX>(dx, place_of(dx, b), sa, sb);
+    else mm_cut<T, DW>(dw, place_of(dw, b - n), sa, sb);
 }
 
 // The splits' partial sums, joined in their order. FWD: both projections of
-// eight columns, then as the product's epilogue; else `batch` results.
+// eight columns, then as the product's epilogue.
 template <class T>
-__global__ __launch_bounds__(256) void k_gate_join_fwd(const Product q, int splits) {
+__global__ __launch_bounds__(256) void k_gate_join_fwd(const Product q) {
     const int per = (q.N + 7) / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / per;
     const int n = (int)(i - m * per) * 8, left = q.N - n;
@@ -679,7 +725,7 @@ __global__ __launch_bounds__(256) void k_gate_join_fwd(const Product q, int spli
     const int64_t MN = q.M * q.N, at = m * q.N + n;
     float g[8] = {}, u[8] = {}, o[8];
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
+    for (int s = 0; s < q.splits; ++s) {
         const Raw8<float> a = load8n(q.part + s * 2 * MN + at, left, 0.f);
         const Raw8<float> b = load8n(q.part + (s * 2 + 1) * MN + at, left, 0.f);
 #pragma unroll
@@ -697,16 +743,21 @@ __global__ __launch_bounds__(256) void k_gate_join_fwd(const Product q, int spli
     }
 }
 
+// The backward's: dx's in the first dx_groups workgroups, then dWg's and dWu's.
 template <class T>
-__global__ __launch_bounds__(256) void k_gate_join(const Product q, int splits, int batch) {
+__global__ __launch_bounds__(256) void k_gate_join(const Product dx, const Product dw, int dx_groups, int dw_groups) {
+    const bool first = (int)blockIdx.x < dx_groups;
+    const Product& q = first ? dx : dw;
+    const int block = first ? blockIdx.x : blockIdx.x - dx_groups;
+    const int z = first ? 0 : block / dw_groups, batch = first ? 1 : 2;
     const int per = (q.N + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / per;
-    const int n = (int)(i - m * per) * 8, left = q.N - n, z = blockIdx.y;
+    const int64_t i = (int64_t)(block - z * dw_groups) * 256 + threadIdx.x, m = i / per;
+    const int n = (int)(i - m * per) * 8, left = q.N - n;
     if (m >= q.M) return;
     const int64_t MN = q.M * q.N, at = m * q.N + n;
     float o[8] = {};
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
+    for (int s = 0; s < q.splits; ++s) {
         const Raw8<float> a = load8n(q.part + (s * batch + z) * MN + at, left, 0.f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += a.at(e);
@@ -819,35 +870,48 @@ __global__ __launch_bounds__(256) void k_gate_few(const Product q) {
 
 inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// Rows the forward takes without tiles.
-constexpr int64_t kFew = 32;
+// Rows the forward takes without tiles: 16, and 32 but for large 16-bit weights,
+// whose tiles are many enough to keep memory busy by themselves (32 rows bf16:
+// 4096 x 10240 46 us without tiles, 33 with them; 2048 x 8192 19 and 19.5; 512 x 1536
+// 7.6 and 10.1; fp32 4096 x 10240 98 and 111).
+bool few_rows(int32_t dtype, int64_t M, int64_t K, int64_t H) {
+    return M <= 16 || (M <= 32 && (dtype == TT_F32 || K * H <= int64_t(1) << 24));
+}
 
-// How a product is cut: tiles of 256 x 256 when they fill the chip, else of
-// 128 x 128, whose summed length is split when they do not fill it either
-// (two workgroups a CU), eight steps or more a split.
+// How a launch's products are cut: tiles of 256 x 256 when these fill the chip, else
+// of 128 x 128, two of which a CU takes. Summed lengths that are long beside what
+// each of 512 workgroups would get are split into pieces of about that, eight steps
+// or more (for large tiles 32: a partial sum of theirs is written and read again).
 struct Cut {
     bool big;
     int mt, nt, steps, split_steps, splits;
 };
-Cut cut_of(int32_t dtype, Kind kind, int64_t M, int64_t N, int64_t K) {
-    const int batch = kind == DW ? 2 : 1;
-    const int64_t per = kind == FWD ? 2 : 1;   // columns of B of one of D
-    Cut c{};
-    c.steps = (int)((K + kBK - 1) / kBK) * (kind == DX ? 2 : 1);
+struct Sum {   // D [M][N], N counting both projections; summed length in steps; how many of them
+    int64_t M, N, steps, batch;
+};
+template <int N>
+void cut_sums(int32_t dtype, const Sum (&p)[N], Cut (&c)[N]) {
     auto tiles = [&](int64_t t) {
-        c.mt = (int)((M + t - 1) / t);
-        c.nt = (int)((N * per + t - 1) / t);
-        return (int64_t)c.mt * c.nt * batch;
+        int64_t n = 0;
+        for (int i = 0; i < N; ++i) {
+            c[i].mt = (int)((p[i].M + t - 1) / t);
+            c[i].nt = (int)((p[i].N + t - 1) / t);
+            n += (int64_t)c[i].mt * c[i].nt * p[i].batch;
+        }
+        return n;
     };
-    c.big = dtype != TT_F32 && tiles(256) >= 256;
-    c.splits = 1;
-    if (!c.big) {
-        const int64_t n = tiles(128);
-        if (n > 0 && n <= 256) c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / n, c.steps / 8, 64}));
+    const bool big = dtype != TT_F32 && tiles(256) >= 256;
+    if (!big) tiles(128);
+    int64_t work = 0;
+    for (int i = 0; i < N; ++i) work += (int64_t)c[i].mt * c[i].nt * p[i].batch * p[i].steps;
+    const int64_t piece = std::max<int64_t>(big ? 32 : 8, (work + 511) / 512);
+    for (int i = 0; i < N; ++i) {
+        c[i].big = big;
+        c[i].steps = (int)p[i].steps;
+        const int64_t n = std::max<int64_t>(1, std::min<int64_t>(p[i].steps / piece, 64));
+        c[i].split_steps = (int)std::max<int64_t>(1, (p[i].steps + n - 1) / n);
+        c[i].splits = std::max(1, (c[i].steps + c[i].split_steps - 1) / c[i].split_steps);
     }
-    c.split_steps = std::max(1, (c.steps + c.splits - 1) / c.splits);
-    c.splits = std::max(1, (c.steps + c.split_steps - 1) / c.split_steps);
-    return c;
 }
 
 // Where things lie in the workspace (bytes): x and the weights with aligned
@@ -855,11 +919,12 @@ Cut cut_of(int32_t dtype, Kind kind, int64_t M, int64_t N, int64_t K) {
 // du, partial sums.
 struct GateSpace {
     int64_t Kp, Hp;
-    Cut fwd, dx, dw;
-    size_t x, wg, wu, gu, part, forward, backward;
-    GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H)
-        : Kp(up_to(K, kPanel)), Hp(up_to(H, kPanel)), fwd(cut_of(dtype, FWD, M, H, K)), dx(cut_of(dtype, DX, M, K, H)),
-          dw(cut_of(dtype, DW, H, K, M)) {
+    Cut fwd[1], back[2];   // back: dx, dW
+    size_t x, wg, wu, gu, part, part_dx, part_dw, forward, backward;
+    GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H) : Kp(up_to(K, kPanel)), Hp(up_to(H, kPanel)) {
+        const int64_t k = (K + kBK - 1) / kBK, h = (H + kBK - 1) / kBK, m = (M + kBK - 1) / kBK;
+        cut_sums(dtype, {Sum{M, 2 * H, k, 1}}, fwd);
+        cut_sums(dtype, {Sum{M, K, 2 * h, 1}, Sum{H, K, m, 2}}, back);
         size_t at = 0;
         auto take = [&](size_t bytes) {
             const size_t o = at;
@@ -872,13 +937,12 @@ struct GateSpace {
         wu = take(copies ? H * Kp * 2 : 0);
         gu = at;
         part = gu;
-        forward = at + (M <= kFew || fwd.splits == 1 ? 0 : (size_t)fwd.splits * 2 * M * H * 4);
+        forward = at + (few_rows(dtype, M, K, H) || fwd[0].splits == 1 ? 0 : (size_t)fwd[0].splits * 2 * M * H * 4);
         take(M * 2 * Hp * (dtype == TT_F32 ? 4 : 2));
-        backward = at + std::max(dx.splits == 1 ? 0 : (size_t)dx.splits * M * K * 4,
-                                 dw.splits == 1 ? 0 : (size_t)dw.splits * 2 * H * K * 4);
-        part_back = at;
+        part_dx = take(back[0].splits == 1 ? 0 : (size_t)back[0].splits * M * K * 4);
+        part_dw = take(back[1].splits == 1 ? 0 : (size_t)back[1].splits * 2 * H * K * 4);
+        backward = at;
     }
-    size_t part_back;   // partial sums of the backward (`part`: the forward's)
 };
 
 struct GateArgs {
@@ -891,28 +955,48 @@ struct GateArgs {
     hipStream_t s;
 };
 
-template <class T, Kind KIND>
-tt_status product(Product q, const Cut& c, char* part, hipStream_t s) {
-    const int batch = KIND == DW ? 2 : 1;
+void cut_product(Product& q, const Cut& c, char* part) {
     q.mt = c.mt;
     q.nt = c.nt;
     q.steps = c.steps;
     q.split_steps = c.split_steps;
+    q.splits = c.splits;
     q.part = c.splits > 1 ? (float*)part : nullptr;
-    const dim3 grid((unsigned)(q.mt * q.nt), (unsigned)c.splits, batch), block(256);
+}
+
+template <class T>
+tt_status forward_product(const Product& q, bool big, hipStream_t s) {
+    const dim3 grid((unsigned)(q.mt * q.nt * q.splits)), block(256);
     if constexpr (sizeof(T) == 4) {
-        TT_LAUNCH(nullptr, "k_gate_mm_cut", s, (k_gate_mm_cut<T, KIND>), grid, block, 0, s, q);
+        TT_LAUNCH(nullptr, "k_gate_mm_cut", s, (k_gate_mm_cut<T>), grid, block, 0, s, q);
     } else {
-        auto k = c.big ? k_gate_mm<T, KIND, 2, 2, 8, 8> : k_gate_mm<T, KIND, 2, 2, 4, 4>;
+        auto k = big ? k_gate_mm<T, 2, 2, 8, 8> : k_gate_mm<T, 2, 2, 4, 4>;
         TT_LAUNCH(nullptr, "k_gate_mm", s, k, grid, block, 0, s, q);
     }
     TT_LAUNCH_CHECK();
-    if (c.splits > 1) {
+    if (q.splits > 1) {
         const unsigned g = grid_for(q.M * ((q.N + 7) / 8), 256);
-        if constexpr (KIND == FWD)
-            TT_LAUNCH(nullptr, "k_gate_join_fwd", s, (k_gate_join_fwd<T>), dim3(g), dim3(256), 0, s, q, c.splits);
-        else
-            TT_LAUNCH(nullptr, "k_gate_join", s, (k_gate_join<T>), dim3(g, batch), dim3(256), 0, s, q, c.splits, batch);
+        TT_LAUNCH(nullptr, "k_gate_join_fwd", s, (k_gate_join_fwd<T>), dim3(g), dim3(256), 0, s, q);
+        TT_LAUNCH_CHECK();
+    }
+    return TT_OK;
+}
+
+template <class T>
+tt_status backward_products(const Product& dx, const Product& dw, bool big, hipStream_t s) {
+    const dim3 grid((unsigned)(dx.mt * dx.nt * dx.splits + dw.mt * dw.nt * dw.splits * 2)), block(256);
+    if constexpr (sizeof(T) == 4) {
+        TT_LAUNCH(nullptr, "k_gate_mm_cut_back", s, (k_gate_mm_cut_back<T>), grid, block, 0, s, dx, dw);
+    } else {
+        auto k = big ? k_gate_mm_back<T, 2, 2, 8, 8> : k_gate_mm_back<T, 2, 2, 4, 4>;
+        TT_LAUNCH(nullptr, "k_gate_mm_back", s, k, grid, block, 0, s, dx, dw);
+    }
+    TT_LAUNCH_CHECK();
+    auto groups = [](const Product& q) { return q.splits > 1 ? (int)grid_for(q.M * ((q.N + 7) / 8), 256) : 0; };
+    const int gx = groups(dx), gw = groups(dw);
+    if (gx + gw > 0) {
+        TT_LAUNCH(nullptr, "k_gate_join", s, (k_gate_join<T>), dim3((unsigned)(gx + 2 * gw)), dim3(256), 0, s, dx, dw,
+                  gx, gw);
         TT_LAUNCH_CHECK();
     }
     return TT_OK;
@@ -975,7 +1059,7 @@ tt_status gate_forward(const GateArgs& a, const GateSpace& sp) {
     q.M = a.M; q.N = (int)a.H; q.K = a.K;
     q.out = a.out; q.ldo = a.ldout;
     q.gate = a.gate; q.up = a.up; q.act = a.act;
-    if (a.M <= kFew) {
+    if (few_rows(sizeof(T) == 4 ? TT_F32 : TT_BF16, a.M, a.K, a.H)) {
         auto k = a.M <= 16 ? k_gate_few<T, 1> : k_gate_few<T, 2>;
         TT_LAUNCH(nullptr, "k_gate_few", a.s, k, dim3(grid_for(a.H, 16)), dim3(256), 0, a.s, q);
         TT_LAUNCH_CHECK();
@@ -987,7 +1071,8 @@ tt_status gate_forward(const GateArgs& a, const GateSpace& sp) {
     q.a = in.x; q.b = in.wg; q.b2 = in.wu;
     q.lda = in.ldx; q.ldb = in.ldw;
     q.pa = in.px; q.pb = in.pw;
-    return product<T, FWD>(q, sp.fwd, a.ws + sp.part, a.s);
+    cut_product(q, sp.fwd[0], a.ws + sp.part);
+    return forward_product<T>(q, sp.fwd[0].big, a.s);
 }
 
 template <class T>
@@ -1008,16 +1093,17 @@ tt_status gate_backward(const GateArgs& a, const GateSpace& sp) {
                   dim3((unsigned)((a.M + 15) / 16 * ((sp.Hp / kPanel + 3) / 4))), dim3(256), 0, a.s, a.gate, a.up,
                   (const T*)a.dout, a.lddout, a.M, (int)a.H, (int)sp.Hp, panel, a.act, gu);
         TT_LAUNCH_CHECK();
-        q.b = in.wg; q.b2 = in.wu; q.ldb = in.ldw;
-        q.M = a.M; q.N = (int)a.K; q.K = a.H;
-        q.out = a.dx; q.ldo = a.lddx;
-        st = product<T, DX>(q, sp.dx, a.ws + sp.part_back, a.s);
-        if (st != TT_OK) return st;
     }
-    q.b = in.x; q.b2 = nullptr; q.ldb = in.ldx;
-    q.M = a.H; q.N = (int)a.K; q.K = a.M;
-    q.out = a.dwg; q.out2 = a.dwu; q.ldo = a.K;
-    return product<T, DW>(q, sp.dw, a.ws + sp.part_back, a.s);
+    Product dx = q, dw = q;
+    dx.b = in.wg; dx.b2 = in.wu; dx.ldb = in.ldw;
+    dx.M = a.M; dx.N = (int)a.K; dx.K = a.H;
+    dx.out = a.dx; dx.ldo = a.lddx;
+    cut_product(dx, sp.back[0], a.ws + sp.part_dx);
+    dw.b = in.x; dw.ldb = in.ldx;
+    dw.M = a.H; dw.N = (int)a.K; dw.K = a.M;
+    dw.out = a.dwg; dw.out2 = a.dwu; dw.ldo = a.K;
+    cut_product(dw, sp.back[1], a.ws + sp.part_dw);
+    return backward_products<T>(dx, dw, sp.back[0].big, a.s);
 }
 
 tt_status gate_by_type(int32_t dtype, const GateArgs& a, bool backward) {
