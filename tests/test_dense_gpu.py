@@ -233,6 +233,15 @@ def test_gate_large_tiles(dt, m, k, h):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("m,k,h", [(4000, 520, 2000), (500, 264, 9000), (3000, 1032, 1100), (8200, 264, 300)])
+def test_gate_tiles_of_each_size(dt, m, k, h):
+    """Rows and columns for one round of the largest tiles, for the middle ones, and few rows beside many columns."""
+    ins = gate_inputs(m, k, h, dt)
+    for a, b in zip(check_gate(*ins, "silu"), run_gate(*ins, "silu")):
+        assert torch.equal(a, b)
+
+
 def test_gate_fp32_range():
     """fp32 operands keep their range: products of very large and very small values."""
     x, wg, wu, d = gate_inputs(70, 128, 64, F32)
