@@ -1016,39 +1016,42 @@ struct Inputs {
 template <class T>
 tt_status aligned_inputs(Inputs& in, const GateArgs& a, const GateSpace& sp, bool panels) {
     in = Inputs{a.x, a.wg, a.wu, a.ldx, kPanel, a.K, kPanel};
-    if (sizeof(T) == 4) return TT_OK;
-    const bool pays = panels && a.M * a.H / (a.M + 2 * a.H) >= 2000;
-    const bool x = pays || a.K % 8 != 0 || a.ldx % 8 != 0 || ((uintptr_t)a.x & 15) != 0;
-    const bool w = pays || a.K % 8 != 0 || (((uintptr_t)a.wg | (uintptr_t)a.wu) & 15) != 0;
-    Align c{};
-    c.cols = (int)a.K;
-    c.up = (int)sp.Kp;
-    c.panel = panels ? kPanel : (int)up_to(a.K, 8);
-    int n = 0;
-    auto take = [&](const void*& p, int64_t ld, int64_t rows, size_t at) {
-        c.src[n] = p;
-        c.ld[n] = ld;
-        c.rows[n] = rows;
-        c.dst[n++] = a.ws + at;
-        p = a.ws + at;
-    };
-    if (x && a.M > 0) {
-        take(in.x, a.ldx, a.M, sp.x);
-        in.ldx = c.panel;
-        if (panels) in.px = a.M * kPanel;
+    if constexpr (sizeof(T) == 4) {
+        return TT_OK;
+    } else {
+        const bool pays = panels && a.M * a.H / (a.M + 2 * a.H) >= 2000;
+        const bool x = pays || a.K % 8 != 0 || a.ldx % 8 != 0 || ((uintptr_t)a.x & 15) != 0;
+        const bool w = pays || a.K % 8 != 0 || (((uintptr_t)a.wg | (uintptr_t)a.wu) & 15) != 0;
+        Align c{};
+        c.cols = (int)a.K;
+        c.up = (int)sp.Kp;
+        c.panel = panels ? kPanel : (int)up_to(a.K, 8);
+        int n = 0;
+        auto take = [&](const void*& p, int64_t ld, int64_t rows, size_t at) {
+            c.src[n] = p;
+            c.ld[n] = ld;
+            c.rows[n] = rows;
+            c.dst[n++] = a.ws + at;
+            p = a.ws + at;
+        };
+        if (x && a.M > 0) {
+            take(in.x, a.ldx, a.M, sp.x);
+            in.ldx = c.panel;
+            if (panels) in.px = a.M * kPanel;
+        }
+        if (w) {
+            take(in.wg, a.K, a.H, sp.wg);
+            take(in.wu, a.K, a.H, sp.wu);
+            in.ldw = c.panel;
+            if (panels) in.pw = a.H * kPanel;
+        }
+        if (n == 0) return TT_OK;
+        const int64_t rows = std::max(c.rows[0], c.rows[n - 1]);
+        TT_LAUNCH(nullptr, "k_gate_align", a.s, (k_gate_align<T>),
+                  dim3((unsigned)((rows + 15) / 16 * ((sp.Kp / kPanel + 3) / 4)), n), dim3(256), 0, a.s, c);
+        TT_LAUNCH_CHECK();
+        return TT_OK;
     }
-    if (w) {
-        take(in.wg, a.K, a.H, sp.wg);
-        take(in.wu, a.K, a.H, sp.wu);
-        in.ldw = c.panel;
-        if (panels) in.pw = a.H * kPanel;
-    }
-    if (n == 0) return TT_OK;
-    const int64_t rows = std::max(c.rows[0], c.rows[n - 1]);
-    TT_LAUNCH(nullptr, "k_gate_align", a.s, (k_gate_align<T>),
-              dim3((unsigned)((rows + 15) / 16 * ((sp.Kp / kPanel + 3) / 4)), n), dim3(256), 0, a.s, c);
-    TT_LAUNCH_CHECK();
-    return TT_OK;
 }
 
 template <class T>

@@ -467,6 +467,44 @@ def operators_once(seed):
     return [x, dy, xs, xf, z], call, outs
 
 
+def far(t, stride):
+    """The same rows `stride` elements apart."""
+    v = torch.empty((t.shape[0] - 1) * stride + t.shape[1], dtype=t.dtype, device=DEV).as_strided(t.shape, (stride, 1))
+    return v.copy_(t)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie more than 2^31 elements (2^32 bytes) into their buffers: the bits of near rows."""
+    x, dy, w = rand(3, 200, seed=1, dt=BF16), rand(3, 200, seed=2, dt=BF16), rand(200, seed=3)
+    got = [far(torch.empty_like(x), 1 << 30) for _ in range(2)]
+    want = [torch.empty_like(x) for _ in range(2)]
+    for (y, dx), (a, b) in ((got, (far(x, 1 << 30), far(dy, 1 << 30))), (want, (x, dy))):
+        mean, rstd = torch.empty(3, device=DEV), torch.empty(3, device=DEV)
+        tte.tt_emb_norm_forward(a, w, None, y, mean, rstd)
+        tte.tt_emb_norm_backward(a, w, mean, rstd, b, dx, torch.empty_like(w))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    z = rand(3, 20000, seed=4, dt=F16)
+    ids, tl, rw = teacher(3, 20000, 30, seed=5)
+    loss = [torch.empty(3, device=DEV) for _ in range(2)]
+    dz, dz2 = far(torch.empty_like(z), 1 << 30), torch.empty_like(z)
+    tte.tt_emb_distill_train(far(z, 1 << 30), ids, tl, rw, loss[0], dz, temperature=2.0)
+    tte.tt_emb_distill_train(z, ids, tl, rw, loss[1], dz2, temperature=2.0)
+    assert torch.equal(*loss) and torch.equal(dz, dz2)
+    del got, dz
+    x, wg, wu, d = gate_inputs(1100, 72, 96, BF16)
+    outs = []
+    for a, b in ((far(x, 1 << 21), far(d, 1 << 21)), (x, d)):
+        new = (lambda t: far(torch.empty_like(t), 1 << 21)) if a is not x else torch.empty_like
+        out, dx, g, u = new(d), new(x), torch.empty(1100, 96, device=DEV), torch.empty(1100, 96, device=DEV)
+        dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
+        tte.tt_emb_gate_forward(a, wg, wu, out, g, u)
+        tte.tt_emb_gate_backward(a, wg, wu, g, u, b, dx, dwg, dwu)
+        outs.append((out, g, u, dx, dwg, dwu))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
 def test_same_bits_on_every_run():
     _, call, outs = operators_once(10)
     call()
