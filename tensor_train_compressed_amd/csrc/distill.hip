@@ -8,8 +8,10 @@
 //
 // An entry is absent when its id is outside [0, V) or its logit is -inf; a row
 // whose list has no entry has loss 0 and gradient 0. Everything is held in
-// fp32; exponents are formed as (z - max) * (log2 e / t), the difference first,
-// so that the terms that matter (z near max) carry no error of a large product.
+// fp32. Exponents are formed as c z - [c max], c = log2 e / t, in one fused operation
+// from the exact product and the rounded [c max]: what that rounding adds is common
+// to every term of a row and leaves with the sum, so that the terms that matter (z
+// near max) carry no error of a large product.
 //
 // Bound by memory: the logits are read and the gradient is written, each once
 // where both are formed in one call. A row is cut into chunks of up to 16,384 classes,
@@ -17,8 +19,8 @@
 // of exponentials meet in the workspace, where each workgroup of the row waits
 // for the others' before it writes its part of the gradient. The workgroups of
 // a CU are at different steps, which keeps memory busy while some form
-// exponentials (two a class, about half the time that memory needs). 4096 x 131072 bf16:
-// 370 us, 5.8 TB/s; 96 x 10^6 fp32: 180 us, 4.3 TB/s.
+// exponentials (two a class; the vector time is near the memory's). 4096 x 131072 bf16:
+// 375 us, 5.7 TB/s; 96 x 10^6 fp32: 176 us, 4.4 TB/s.
 #include "tt_dense.h"
 
 namespace tt {
@@ -58,10 +60,29 @@ struct alignas(8) MaxSum {
 // 2^x by the hardware instruction; results below 2^-126 are 0.
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// [c m], rounded before anything else is done with it.
+__device__ __forceinline__ float times(float m, float c) {
+    float mc = m * c;
+    asm("" : "+v"(mc));
+    return mc;
+}
+// Maxima whose product with c may overflow (a row of the type's lowest values):
+// there the difference comes first.
+__device__ __forceinline__ bool is_far(float mc) { return !(fabsf(mc) <= 1e30f); }
+
+// f(exponent), exponent(z) that of z at the maximum m; the same for the workgroup.
+template <class F>
+__device__ __forceinline__ void at_maximum(float m, float c, F f) {
+    const float mc = times(m, c);
+    if (is_far(mc)) f([=](float z) { return (z - m) * c; });
+    else f([=](float z) { return fmaf(z, c, -mc); });
+}
+
 // A part's sum at the maximum m of the whole (a part of -inf only has s = 0
 // and joins without a NaN).
 __device__ __forceinline__ float at_max(MaxSum a, float m, float c) {
-    return a.m == m ? a.s : a.s * pow2((a.m - m) * c);
+    const float from = times(a.m, c), to = times(m, c);
+    return a.m == m ? a.s : a.s * pow2(is_far(from) || is_far(to) ? (a.m - m) * c : from - to);
 }
 
 __device__ __forceinline__ float block_max(float v, float* sm) {
@@ -101,14 +122,15 @@ __device__ __forceinline__ MaxSum chunk_stats(Raw8<T> (&r)[kVecs], int n, float 
     }
     keep_raw(r);
     m = block_max(m, sm);
-    const float shift = m == -INFINITY ? 0.f : m;
     float s = 0.f;
+    at_maximum(m == -INFINITY ? 0.f : m, c, [&](auto exponent) {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-        if (v * kPiece < n)
+        for (int v = 0; v < kVecs; ++v) {
+            if (v * kPiece < n)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += pow2((r[v].at(e) - shift) * c);
-    }
+                for (int e = 0; e < 8; ++e) s += pow2(exponent(r[v].at(e)));
+        }
+    });
     return {m, block_sum(s, sm)};
 }
 
@@ -137,6 +159,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_stats(const T* __restrict_
 struct List {
     alignas(16) int32_t id[kMaxTop];   // -1 up to a multiple of 4 past the list's end
     alignas(16) float p[kMaxTop];      // 2^x / sum
+    float all[kMaxTop];                // of the entry's class, where it lies in this workgroup's chunk
     float x[kMaxTop];                  // (logit - the largest) * c, in powers of two
 };
 
@@ -178,18 +201,38 @@ __device__ __forceinline__ float row_loss(const List& l, int top, float lsum, co
                                           float t, float c, float* sm) {
     const float log2s = log2f(a.s);
     float d = 0.f;
-    for (int k = threadIdx.x; k < top; k += kThreads) {
-        const float p = l.p[k];
-        if (l.id[k] < 0 || p == 0.f) continue;   // p log p -> 0
-        d += p * ((l.x[k] - lsum) - (((float)zrow[l.id[k]] - a.m) * c - log2s));
-    }
+    at_maximum(a.m, c, [&](auto exponent) {
+        for (int k = threadIdx.x; k < top; k += kThreads) {
+            const float p = l.p[k];
+            if (l.id[k] < 0 || p == 0.f) continue;   // p log p -> 0
+            d += p * ((l.x[k] - lsum) - (exponent((float)zrow[l.id[k]]) - log2s));
+        }
+    });
     return t * t * 0.6931471805599453f * block_sum(d, sm);
 }
 
+// The sums of p over each class that the list names in this chunk (a class may be
+// listed more than once).
+__device__ __forceinline__ void list_sums(List& l, int top, int64_t c0, int n) {
+    for (int j = threadIdx.x; j < top; j += kThreads) {
+        const int me = l.id[j];
+        if (me < 0 || me < c0 || me >= c0 + n) continue;
+        float p = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < top; i += 4) {
+            const int4 k = *reinterpret_cast<const int4*>(l.id + i);
+            const float4 q = *reinterpret_cast<const float4*>(l.p + i);
+            p += (k.x == me ? q.x : 0.f) + (k.y == me ? q.y : 0.f) + (k.z == me ? q.z : 0.f) + (k.w == me ? q.w : 0.f);
+        }
+        l.all[j] = p;
+    }
+}
+
 // w t q at every class of a chunk, then the list's classes again with their p
-// taken off, once the chunk is written. Measured both ways at 4096 x 131072 bf16: 374 us;
-// 442 with p taken off before the one store (registers hold it), and 414 with each
-// thread writing its own listed classes again without a barrier.
+// (l.all, formed while the row's other workgroups finish: 96 x 10^6 fp32 183 -> 176 us,
+// 194 -> 169 with lists that spread over all classes) taken off, once the chunk is
+// written. Measured at 4096 x 131072 bf16: 375 us; 442 with p taken off before the one
+// store (registers hold it), 414 with each thread writing its own listed classes again.
 template <class T>
 __device__ __forceinline__ void chunk_grad(Raw8<T> (&r)[kVecs], const T* __restrict__ zc, int64_t c0, int n,
                                            const List& l, int top, MaxSum a, float wt, float c, bool apart,
@@ -198,34 +241,34 @@ __device__ __forceinline__ void chunk_grad(Raw8<T> (&r)[kVecs], const T* __restr
     for (int j = threadIdx.x; j < top; j += kThreads) any |= l.id[j] >= 0;
     const bool some = __syncthreads_or(any);
     keep_raw(r);
-    const float inv = 1.f / a.s;
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-        if (v * kPiece >= n) continue;
+    const float scale = wt * (1.f / a.s);
+    auto write = [&](int v, const float (&g)[8]) {
         const int o = v * kPiece + threadIdx.x * 8;
-        float g[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            g[e] = some ? wt * (pow2((r[v].at(e) - a.m) * c) * inv) : 0.f;
         if (apart) store8n_apart(dc + o, g, n - o);
         else store8n(dc + o, g, n - o);
+    };
+    if (!some) {   // 0 whatever the logits are
+        const float g[8] = {};
+        for (int v = 0; v * kPiece < n; ++v) write(v, g);
+        return;
     }
-    __syncthreads();   // the list's classes are written after the whole chunk
-    for (int j = threadIdx.x; j < top; j += kThreads) {
-        const int64_t id = (int64_t)l.id[j] - c0;
-        if (l.id[j] < 0 || id < 0 || id >= n) continue;
-        // a class that is listed more than once: every entry of it writes the same sum
-        // (four entries a step: this scan is a few threads' latency at the workgroup's end)
-        float p = 0.f;
-        const int me = l.id[j];
-#pragma unroll 4
-        for (int i = 0; i < top; i += 4) {
-            const int4 k = *reinterpret_cast<const int4*>(l.id + i);
-            const float4 q = *reinterpret_cast<const float4*>(l.p + i);
-            p += (k.x == me ? q.x : 0.f) + (k.y == me ? q.y : 0.f) + (k.z == me ? q.z : 0.f) + (k.w == me ? q.w : 0.f);
+    at_maximum(a.m, c, [&](auto exponent) {
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            if (v * kPiece >= n) continue;
+            float g[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = scale * pow2(exponent(r[v].at(e)));
+            write(v, g);
         }
-        dc[id] = (T)(wt * (pow2(((float)zc[id] - a.m) * c) * inv - p));
-    }
+        __syncthreads();   // the list's classes are written after the whole chunk
+        for (int j = threadIdx.x; j < top; j += kThreads) {
+            const int64_t id = (int64_t)l.id[j] - c0;
+            if (l.id[j] < 0 || id < 0 || id >= n) continue;
+            const float p = l.all[j];   // every entry of a class writes the same
+            dc[id] = (T)(scale * pow2(exponent((float)zc[id])) - wt * p);
+        }
+    });
 }
 
 // One workgroup a row: joins the chunks' statistics, forms the row's loss.
@@ -262,6 +305,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const T* __restrict__
     Raw8<T> r[kVecs];
     chunk_load(r, z + row * ldz + c0, n);
     list_load(l, ids + row * top, top_logits + row * top, top, V, c, sm);
+    list_sums(l, top, c0, n);
     chunk_grad(r, z + row * ldz + c0, c0, n, l, top, stats[row], t * row_weight[row], c, apart,
                dz + row * lddz + c0);
 }
@@ -294,10 +338,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void k_distill_ro
     chunk_load(r, zr + c0, n);
     const float lsum = list_load(l, ids + row * top, top_logits + row * top, top, V, c, sm);
     MaxSum a = chunk_stats(r, n, c, sm);
+    if (cut.chunks > 1 && threadIdx.x == 0)
+        __hip_atomic_store(part + row * cut.chunks + mine, __builtin_bit_cast(uint64_t, a), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    if (GRAD) list_sums(l, top, c0, n);
     if (cut.chunks > 1) {
         uint64_t* rp = part + row * cut.chunks;
-        if (threadIdx.x == 0)
-            __hip_atomic_store(rp + mine, __builtin_bit_cast(uint64_t, a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         uint64_t p = kNoPart;
         const bool polls = (int)threadIdx.x < cut.chunks;
         for (int i = 0; i < spins && polls && p == kNoPart; ++i) {

@@ -399,6 +399,20 @@ def test_distill_masked_classes(v):
         assert bool(torch.isfinite(loss[[0, 1, 2, 5]]).all()) and bool(torch.isfinite(dz[[0, 1, 2, 5]]).all())
 
 
+@TYPES
+@pytest.mark.parametrize("v", [300, 40000])
+def test_distill_lowest_values(dt, v):
+    """Rows masked with the type's lowest value as a whole, but for one class, and in part: like any logits."""
+    low = torch.finfo(dt).min
+    z = rand(4, v, seed=1)
+    z[0] = low
+    z[1], z[1, 5] = low, 1.0
+    z[2, v // 2:] = low
+    z[3], z[3, 7] = low, -low                      # the type's largest
+    ids = torch.tensor([[0, 1, v - 1, 9], [5, 5, 5, 5], [0, 1, 2, 3], [7, 7, 7, 7]], device=DEV)
+    check_distill(z.to(dt), ids, rand(4, 4, seed=2), torch.ones(4, device=DEV), 1.0)
+
+
 def test_distill_nan_rows_stay_apart():
     z = rand(4, 40000, seed=1)
     ids, tl, w = teacher(4, 40000, 9, seed=3, holes=False)
