@@ -152,14 +152,15 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_fwd(
     }
 }
 
-// The workgroup's sums of dw and db go to part[blockIdx.x][0 or 1][dim].
+// The workgroup's sums of dw and db go to part[blockIdx.x][0 or 1][dim], those of an
+// only workgroup straight to dweight and dbias.
 // 16384 x 4096 bf16: 83 us, 4.8 TB/s, what a large copy reaches; with the next two
 // rows under way instead of one the same, and 32768 x 128 fp32 10.6 us for 8.9.
 template <class T, class WT, int TPR, int E>
 __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_bwd(
     const T* __restrict__ x, int64_t ldx, const WT* __restrict__ weight, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, const T* __restrict__ dy, int64_t lddy, T* __restrict__ dx, int64_t lddx,
-    float* __restrict__ part, int64_t rows, int dim) {
+    float* __restrict__ part, WT* __restrict__ dweight, WT* __restrict__ dbias, int64_t rows, int dim) {
     constexpr int GPB = norm_block<TPR>() / TPR, NV = E / 8;
     __shared__ float sm[2][2][16];
     int slot = 0;
@@ -234,6 +235,11 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_bwd(
         }
     }
     float* pw = part + (int64_t)blockIdx.x * 2 * dim;
+    auto put = [&](int k, int c, float a) {
+        if (gridDim.x > 1) pw[k * dim + c] = a;
+        else if (k == 0) dweight[c] = (WT)a;
+        else if (dbias) dbias[c] = (WT)a;
+    };
     if constexpr (GPB == 1) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -241,8 +247,8 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_bwd(
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (c + e < dim) {
-                    pw[c + e] = dw[v * 8 + e];
-                    pw[dim + c + e] = db[v * 8 + e];
+                    put(0, c + e, dw[v * 8 + e]);
+                    put(1, c + e, db[v * 8 + e]);
                 }
         }
     } else {
@@ -266,7 +272,7 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_bwd(
             float a = 0.f;
 #pragma unroll
             for (int j = 0; j < GPB; ++j) a += sw[j][k][c];
-            pw[k * dim + c] = a;
+            put(k, c, a);
         }
     }
 }
@@ -293,12 +299,16 @@ __global__ __launch_bounds__(1024) void k_norm_wgrad(const float* __restrict__ p
 }
 
 // Workgroups of the backward (and parts of dw, db): two of 256 threads a CU,
-// fewer of the larger ones, so that the parts stay small beside the rows.
+// fewer of the larger ones, so that the parts stay small beside the rows. A single
+// one for a few rows a group, which needs no second launch: 64 x 128 fp32 11.3 ->
+// 8.8 us, 4 x 4096 11.4 -> 10.3 (but 32 x 1000 10.9 -> 13.5, 4 x 16384 25.0 -> 27.9).
 inline int64_t norm_bwd_blocks(int64_t rows, int64_t dim) {
     const NormShape sh = norm_shape(dim);
     const int64_t gpb = sh.threads < 256 ? 256 / sh.threads : 1;
     const int64_t most = sh.threads <= 512 ? 512 : 256;
-    return std::min(most, (rows + gpb - 1) / gpb);
+    const int64_t n = (rows + gpb - 1) / gpb;
+    const int64_t one = sh.threads <= 32 ? 8 : sh.threads <= 256 ? 4 : 1;
+    return n <= one ? std::min<int64_t>(n, 1) : std::min(most, n);
 }
 
 inline int64_t norm_fwd_blocks(int64_t rows, int64_t dim) {
@@ -332,8 +342,9 @@ tt_status norm_launch(const NormArgs& a, bool backward) {
     if (grid) {
         TT_LAUNCH(nullptr, "k_norm_bwd", a.s, (k_norm_bwd<T, WT, TPR, E>), dim3(grid), dim3(BLOCK), 0, a.s,
                   (const T*)a.x, a.ldx, (const WT*)a.weight, a.mean, a.rstd, (const T*)a.dy, a.lddy, (T*)a.dx,
-                  a.lddx, a.part, a.rows, (int)a.dim);
+                  a.lddx, a.part, (WT*)a.dweight, (WT*)a.dbias, a.rows, (int)a.dim);
         TT_LAUNCH_CHECK();
+        if (grid == 1) return TT_OK;
     }
     TT_LAUNCH(nullptr, "k_norm_wgrad", a.s, (k_norm_wgrad<WT>), dim3(grid_for(a.dim, 16), a.dbias ? 2 : 1),
               dim3(1024), 0, a.s, a.part, (int)grid, (int)a.dim, (WT*)a.dweight, (WT*)a.dbias);

@@ -95,6 +95,15 @@ def test_norm_fp32_weights_no_bias(dt, dim):
     check_norm(rand(70, dim, seed=1, dt=dt), w, None, rand(70, dim, seed=2, dt=dt))
 
 
+@TYPES
+@pytest.mark.parametrize("rows,dim", [(127, 100), (129, 100), (32, 900), (33, 900), (4, 4000), (5, 4000), (2, 16000)])
+def test_norm_around_one_workgroup(dt, rows, dim):
+    """Batches that one workgroup takes, and the next larger ones."""
+    w = 1 + 0.1 * rand(dim, seed=4)
+    b = rand(dim, seed=5)
+    check_norm(rand(rows, dim, seed=1, dt=dt), w.to(dt), b.to(dt), rand(rows, dim, seed=2, dt=dt))
+
+
 def test_norm_many_rows():
     """More rows than one pass of the workgroups takes."""
     x, dy = rand(40000, 128, seed=1), rand(40000, 128, seed=2)
