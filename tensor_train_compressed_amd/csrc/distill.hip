@@ -9,9 +9,11 @@
 // An entry is absent when its id is outside [0, V) or its logit is -inf; a row
 // whose list has no entry has loss 0 and gradient 0. Everything is held in
 // fp32. Exponents are formed as c z - [c max], c = log2 e / t, in one fused operation
-// from the exact product and the rounded [c max]: what that rounding adds is common
-// to every term of a row and leaves with the sum, so that the terms that matter (z
-// near max) carry no error of a large product.
+// from the exact product and the rounded [c max]: what that rounding adds, half a step
+// of the product, is common to every term of a part and leaves with its sum, so that
+// the terms that matter (z near max) carry no error of a large product. That holds
+// while the half step is small beside the range of 2^x: past |c max| = 2^24, where it
+// is 1 and grows with the product, the difference z - max comes first.
 //
 // Bound by memory: the logits are read and the gradient is written, each once
 // where both are formed in one call. A row is cut into chunks of up to 16,384 classes,
@@ -54,7 +56,7 @@ constexpr int64_t kMaxClasses = int64_t(1) << 30;
 constexpr float kMinT = 1e-18f, kMaxT = 1e18f;            // t^2 and 1/t within fp32's range
 
 struct alignas(8) MaxSum {
-    float m, s;   // the largest z, and sum 2^((z - m) c); m = -inf goes with s = 0
+    float m, s;   // the largest z, and the sum of 2^exponent(z) at it; m = -inf goes with s = 0
 };
 
 // 2^x by the hardware instruction; results below 2^-126 are 0.
@@ -66,9 +68,10 @@ __device__ __forceinline__ float times(float m, float c) {
     asm("" : "+v"(mc));
     return mc;
 }
-// Maxima whose product with c may overflow (a row of the type's lowest values):
-// there the difference comes first.
-__device__ __forceinline__ bool is_far(float mc) { return !(fabsf(mc) <= 1e30f); }
+// Where the difference from the maximum comes first: products whose rounding would
+// move every term by more than 2^(1/2), or overflow (rows or chunks masked with a large
+// finite value; low temperatures).
+__device__ __forceinline__ bool is_far(float mc) { return !(fabsf(mc) <= 16777216.f); }
 
 // f(exponent), exponent(z) that of z at the maximum m; the same for the workgroup.
 template <class F>
@@ -77,12 +80,16 @@ __device__ __forceinline__ void at_maximum(float m, float c, F f) {
     if (is_far(mc)) f([=](float z) { return (z - m) * c; });
     else f([=](float z) { return fmaf(z, c, -mc); });
 }
+// exponent(m): what every exponent of a part with this maximum is too large by.
+__device__ __forceinline__ float excess(float m, float c) {
+    const float mc = times(m, c);
+    return is_far(mc) ? 0.f : fmaf(m, c, -mc);
+}
 
 // A part's sum at the maximum m of the whole (a part of -inf only has s = 0
 // and joins without a NaN).
 __device__ __forceinline__ float at_max(MaxSum a, float m, float c) {
-    const float from = times(a.m, c), to = times(m, c);
-    return a.m == m ? a.s : a.s * pow2(is_far(from) || is_far(to) ? (a.m - m) * c : from - to);
+    return a.m == m ? a.s : a.s * pow2((a.m - m) * c + (excess(m, c) - excess(a.m, c)));
 }
 
 __device__ __forceinline__ float block_max(float v, float* sm) {
