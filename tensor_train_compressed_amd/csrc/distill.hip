@@ -25,6 +25,8 @@
 // 375 us, 5.7 TB/s; 96 x 10^6 fp32: 176 us, 4.4 TB/s.
 #include "tt_dense.h"
 
+#include <atomic>
+
 namespace tt {
 namespace {
 
@@ -391,7 +393,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) void k_distill_ro
 constexpr int64_t kApart = int64_t(64) << 20;
 
 // Polls before a workgroup forms the missing parts itself: about 10 ms.
-constexpr int kSpins = 1 << 15;
+constexpr int kPolls = 1 << 15;
+std::atomic<int> polls{kPolls};
 
 struct DistillArgs {
     const void* z;
@@ -422,7 +425,7 @@ tt_status distill_launch(const DistillArgs& a, const Cut& cut, bool forward, boo
         }
         auto k = backward ? k_distill_row<T, true> : k_distill_row<T, false>;
         TT_LAUNCH(nullptr, "k_distill_row", a.s, k, grid, block, 0, a.s, z, a.ldz, a.V, cut, a.t, c, a.ids,
-                  a.top_logits, a.top, (uint64_t*)a.part, kSpins, a.row_weight, a.loss, backward ? nullptr : a.stats,
+                  a.top_logits, a.top, (uint64_t*)a.part, polls.load(std::memory_order_relaxed), a.row_weight, a.loss, backward ? nullptr : a.stats,
                   apart, (T*)a.dz, a.lddz);
         TT_LAUNCH_CHECK();
         return TT_OK;
@@ -508,6 +511,8 @@ tt_status distill_workspace(DistillArgs& a, int32_t dtype, void* ws, size_t byte
 }  // namespace tt
 
 using namespace tt;
+
+extern "C" int32_t tt_distill_set_polls(int32_t n) { return polls.exchange(n < 0 ? kPolls : n); }
 
 extern "C" size_t tt_emb_distill_workspace_bytes(int32_t dtype, int64_t rows, int64_t classes) {
     if (distill_check(dtype, rows, classes) != TT_OK) return 0;

@@ -11,6 +11,12 @@
 #include <cstddef>
 #include <type_traits>
 
+// Not part of the library's interface; for its tests. How often a workgroup of
+// tt_emb_distill_train polls for the other parts of its row before it forms them
+// itself (negative: the default), for every later call of the process. Returns what
+// it was. Every count gives the same bits.
+extern "C" int32_t tt_distill_set_polls(int32_t n);
+
 namespace tt {
 
 typedef __bf16 bf16;
