@@ -9,8 +9,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from tests import dense_ref as ref  # noqa: E402
-from tests.gpu_helpers import DEV  # noqa: E402
-from tests.test_dense_gpu import BF16, F32, TYPES, check_distill, rand, teacher  # noqa: E402
+from tests.gpu_helpers import DEV, say  # noqa: E402
+from tests.test_dense_gpu import BF16, F32, TYPES, check_distill, rand, run_distill, teacher  # noqa: E402
 
 WIDE = pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 SIZES = pytest.mark.parametrize("v", [300, 40000])      # one chunk a row, and several
@@ -63,3 +63,16 @@ def test_low_temperatures(dt, v, power):
     z = (2 * rand(9, v, seed=1)).to(dt)
     z[1, :] = z[1, :1]                      # all classes alike
     check_distill(z, ids, tl, w + 0.5, 2.0 ** power)
+
+
+@TYPES
+@pytest.mark.parametrize("v,top", [(300, 5), (16384, 64), (16385, 64), (40000, 9), (131072, 300)])
+def test_one_call_gives_the_bits_of_two(dt, v, top):
+    """Forward and backward apart, in one call, and the forward without statistics: the same bits."""
+    ids, tl, w = teacher(7, v, top, seed=v)
+    z = (2 * rand(7, v, seed=1)).to(dt)
+    z[3, :v // 2] = -1e4
+    say("distill bits", dt, v, top)
+    (loss, dz), (loss2, dz2), only = run_distill(z, ids, tl, w, 2.0)
+    assert torch.equal(loss, loss2) and torch.equal(loss, only)
+    assert torch.equal(dz, dz2)
