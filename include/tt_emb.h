@@ -359,7 +359,8 @@ tt_status tt_emb_backward_sgd_cached(tt_emb_plan_t plan, uint64_t kept_token, fl
  * must not overlap inputs or each other.
  *
  * Workspaces are device buffers of the caller's, at least as large as the
- * matching _workspace_bytes call says and 256-byte aligned; they hold nothing
+ * matching _workspace_bytes call says and 256-byte aligned; one sized for some
+ * number of rows serves fewer rows of the same widths and type too. They hold nothing
  * between calls, and calls that may run at the same time need one each. The
  * _workspace_bytes calls are pure host computations and return 0 for sizes
  * that are invalid or unsupported. The calls allocate nothing, wait for

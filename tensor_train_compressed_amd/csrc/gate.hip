@@ -914,17 +914,36 @@ void cut_sums(int32_t dtype, const Sum (&p)[N], Cut (&c)[N]) {
     }
 }
 
+// Bytes that a launch's partial sums take at most, at these sizes and at any smaller M:
+// a product that is split is split into pieces of work / 512 steps or more, so that the
+// tiles and splits of all that are are 512 workgroups at most, and of eight steps or more.
+template <int N>
+size_t partial_bytes(int32_t dtype, const Sum (&p)[N]) {
+    Cut c[N];
+    cut_sums(dtype, p, c);
+    const int64_t tile = c[0].big ? 256 : 128;
+    int64_t sums = 0;
+    for (int i = 0; i < N; ++i) {
+        const int64_t n = std::min<int64_t>(p[i].steps / 8, 64);
+        if (n > 1) sums += n * p[i].batch * p[i].M * p[i].N;
+    }
+    return sums ? up_to(std::min(sums, 512 * tile * tile) * sizeof(float), 256) + 256 * N : 0;   // each rounded up
+}
+
 // Where things lie in the workspace (bytes): x and the weights with aligned
 // rows (16-bit types; used where the caller's are not), the backward's dg and
-// du, partial sums.
+// du, partial sums. forward, backward: what a call of these sizes needs; most:
+// what one of these sizes or of fewer rows does (splits come and go with the rows,
+// all else only grows).
 struct GateSpace {
     int64_t Kp, Hp;
     Cut fwd[1], back[2];   // back: dx, dW
-    size_t x, wg, wu, gu, part, part_dx, part_dw, forward, backward;
+    size_t x, wg, wu, gu, part, part_dx, part_dw, forward, backward, most;
     GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H) : Kp(up_to(K, kPanel)), Hp(up_to(H, kPanel)) {
         const int64_t k = (K + kBK - 1) / kBK, h = (H + kBK - 1) / kBK, m = (M + kBK - 1) / kBK;
-        cut_sums(dtype, {Sum{M, 2 * H, k, 1}}, fwd);
-        cut_sums(dtype, {Sum{M, K, 2 * h, 1}, Sum{H, K, m, 2}}, back);
+        const Sum fwd_sums[1] = {{M, 2 * H, k, 1}}, back_sums[2] = {{M, K, 2 * h, 1}, {H, K, m, 2}};
+        cut_sums(dtype, fwd_sums, fwd);
+        cut_sums(dtype, back_sums, back);
         size_t at = 0;
         auto take = [&](size_t bytes) {
             const size_t o = at;
@@ -937,11 +956,16 @@ struct GateSpace {
         wu = take(copies ? H * Kp * 2 : 0);
         gu = at;
         part = gu;
-        forward = at + (few_rows(dtype, M, K, H) || fwd[0].splits == 1 ? 0 : (size_t)fwd[0].splits * 2 * M * H * 4);
+        const size_t few = 256;
+        forward = std::max(few, at + (few_rows(dtype, M, K, H) || fwd[0].splits == 1
+                                          ? 0 : (size_t)fwd[0].splits * 2 * M * H * 4));
+        most = at + partial_bytes(dtype, fwd_sums);
         take(M * 2 * Hp * (dtype == TT_F32 ? 4 : 2));
+        const size_t parts = at;
         part_dx = take(back[0].splits == 1 ? 0 : (size_t)back[0].splits * M * K * 4);
         part_dw = take(back[1].splits == 1 ? 0 : (size_t)back[1].splits * 2 * H * K * 4);
-        backward = at;
+        backward = std::max(few, at);
+        most = std::max({few, most, parts + partial_bytes(dtype, back_sums)});
     }
 };
 
@@ -1109,8 +1133,10 @@ tt_status gate_backward(const GateArgs& a, const GateSpace& sp) {
     return backward_products<T>(dx, dw, sp.back[0].big, a.s);
 }
 
-tt_status gate_by_type(int32_t dtype, const GateArgs& a, bool backward) {
+tt_status gate_by_type(int32_t dtype, const GateArgs& a, size_t workspace_bytes, bool backward) {
     const GateSpace sp(dtype, a.M, a.K, a.H);
+    if (workspace_bytes < (backward ? sp.backward : sp.forward)) return TT_ERR_WORKSPACE;
+    if (!backward && a.M == 0) return TT_OK;
     if (dtype == TT_F32) return backward ? gate_backward<float>(a, sp) : gate_forward<float>(a, sp);
     if (dtype == TT_BF16) return backward ? gate_backward<bf16>(a, sp) : gate_forward<bf16>(a, sp);
     return backward ? gate_backward<f16>(a, sp) : gate_forward<f16>(a, sp);
@@ -1135,8 +1161,7 @@ using namespace tt;
 
 extern "C" size_t tt_emb_gate_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden) {
     if (gate_check(dtype, rows, dim, hidden) != TT_OK) return 0;
-    const GateSpace sp(dtype, rows, dim, hidden);
-    return std::max<size_t>(256, std::max(sp.forward, sp.backward));
+    return GateSpace(dtype, rows, dim, hidden).most;
 }
 
 extern "C" tt_status tt_emb_gate_forward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate,
@@ -1149,13 +1174,11 @@ extern "C" tt_status tt_emb_gate_forward(int32_t dtype, const void* x, int64_t l
         return TT_ERR_INVALID_ARG;
     if ((rows > 0 && (!x || !out)) || !workspace || ((uintptr_t)workspace & 255) != 0) return TT_ERR_INVALID_ARG;
     if (!stride_ok(ldx)) return TT_ERR_UNSUPPORTED;
-    if (workspace_bytes < tt_emb_gate_workspace_bytes(dtype, rows, dim, hidden)) return TT_ERR_WORKSPACE;
-    if (rows == 0) return TT_OK;
     GateArgs a{};
     a.x = x; a.wg = w_gate; a.wu = w_up; a.out = out;
     a.ldx = ldx; a.ldout = ldout; a.M = rows; a.K = dim; a.H = hidden;
     a.gate = gate; a.up = up; a.act = act; a.ws = (char*)workspace; a.s = (hipStream_t)stream;
-    return gate_by_type(dtype, a, false);
+    return gate_by_type(dtype, a, workspace_bytes, false);
 }
 
 extern "C" tt_status tt_emb_gate_backward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate,
@@ -1171,11 +1194,10 @@ extern "C" tt_status tt_emb_gate_backward(int32_t dtype, const void* x, int64_t 
     if (rows > 0 && (!x || !gate || !up || !dout || !dx)) return TT_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255) != 0) return TT_ERR_INVALID_ARG;
     if (!stride_ok(ldx)) return TT_ERR_UNSUPPORTED;
-    if (workspace_bytes < tt_emb_gate_workspace_bytes(dtype, rows, dim, hidden)) return TT_ERR_WORKSPACE;
     GateArgs a{};
     a.x = x; a.wg = w_gate; a.wu = w_up; a.dout = dout; a.dx = dx; a.dwg = dw_gate; a.dwu = dw_up;
     a.ldx = ldx; a.lddout = lddout; a.lddx = lddx; a.M = rows; a.K = dim; a.H = hidden;
     a.gate = const_cast<float*>(gate); a.up = const_cast<float*>(up);
     a.act = act; a.ws = (char*)workspace; a.s = (hipStream_t)stream;
-    return gate_by_type(dtype, a, true);
+    return gate_by_type(dtype, a, workspace_bytes, true);
 }
