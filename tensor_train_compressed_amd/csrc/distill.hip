@@ -498,12 +498,17 @@ tt_status distill_args(DistillArgs& a, int32_t dtype, const void* z, int64_t ldz
     return TT_OK;
 }
 
+inline size_t workspace_of(int64_t parts) {
+    return std::max<size_t>(256, ((size_t)parts * sizeof(MaxSum) + 255) & ~size_t(255));
+}
+
 // The workspace: the chunks' statistics, then the rows'.
-tt_status distill_workspace(DistillArgs& a, int32_t dtype, void* ws, size_t bytes) {
+tt_status distill_workspace(DistillArgs& a, void* ws, size_t bytes) {
     if (!ws || ((uintptr_t)ws & 255) != 0) return TT_ERR_INVALID_ARG;
-    if (bytes < tt_emb_distill_workspace_bytes(dtype, a.rows, a.V)) return TT_ERR_WORKSPACE;
+    const int64_t parts = a.rows * cut_of(a.rows, a.V).chunks;
+    if (bytes < workspace_of(parts + a.rows)) return TT_ERR_WORKSPACE;
     a.part = (MaxSum*)ws;
-    a.stats = a.part + a.rows * cut_of(a.rows, a.V).chunks;
+    a.stats = a.part + parts;
     return TT_OK;
 }
 
@@ -516,8 +521,10 @@ extern "C" int32_t tt_distill_set_polls(int32_t n) { return polls.exchange(n < 0
 
 extern "C" size_t tt_emb_distill_workspace_bytes(int32_t dtype, int64_t rows, int64_t classes) {
     if (distill_check(dtype, rows, classes) != TT_OK) return 0;
-    const size_t b = (size_t)rows * (size_t)(cut_of(rows, classes).chunks + 1) * sizeof(MaxSum);
-    return std::max<size_t>(256, (b + 255) & ~size_t(255));
+    // what fewer rows, cut into more chunks each, need is no more than this either: theirs
+    // are as few as a row takes, or at most the 1024 they are cut to reach and one a row
+    const int64_t pieces = (classes + kPiece - 1) / kPiece, least = (classes + kChunk - 1) / kChunk;
+    return workspace_of(std::max(rows * least, std::min(rows * ((pieces + 1) / 2), rows + 1024)) + rows);
 }
 
 extern "C" tt_status tt_emb_distill_forward(int32_t dtype, const void* logits, int64_t ld, const int64_t* ids,
@@ -528,7 +535,7 @@ extern "C" tt_status tt_emb_distill_forward(int32_t dtype, const void* logits, i
     tt_status st = distill_args(a, dtype, logits, ld, ids, top_logits, top, temperature, rows, classes, stream);
     if (st != TT_OK) return st;
     if (rows > 0 && !loss) return TT_ERR_INVALID_ARG;
-    if ((st = distill_workspace(a, dtype, workspace, workspace_bytes)) != TT_OK) return st;
+    if ((st = distill_workspace(a, workspace, workspace_bytes)) != TT_OK) return st;
     a.loss = loss;
     a.stats = (MaxSum*)stats;
     return distill_by_type(dtype, a, true, false);
@@ -557,7 +564,7 @@ extern "C" tt_status tt_emb_distill_train(int32_t dtype, const void* logits, int
     tt_status st = distill_args(a, dtype, logits, ld, ids, top_logits, top, temperature, rows, classes, stream);
     if (st != TT_OK) return st;
     if (ldd < classes || (rows > 0 && (!row_weight || !loss || !dlogits))) return TT_ERR_INVALID_ARG;
-    if ((st = distill_workspace(a, dtype, workspace, workspace_bytes)) != TT_OK) return st;
+    if ((st = distill_workspace(a, workspace, workspace_bytes)) != TT_OK) return st;
     a.loss = loss;
     a.row_weight = row_weight;
     a.dz = dlogits;

@@ -30,6 +30,19 @@ def test_gate_workspace_serves_fewer_rows():
             rising([(m, tte.tt_emb_gate_workspace_bytes(dt, m, dim, hidden)) for m in row_counts(rng)])
 
 
+def test_distill_workspace_serves_fewer_rows():
+    rng = random.Random(4)
+    for classes in [1, 2048, 4096, 4097, 16384, 16385, 50021, 131072, 1000000, 1 << 22] + \
+            [rng.randrange(1, 300000) for _ in range(20)]:
+        for dt in (F32, F16):
+            rising([(m, tte.tt_emb_distill_workspace_bytes(dt, m, classes)) for m in range(1, 2100)])
+
+
+def test_norm_workspace_serves_fewer_rows():
+    for dim in (1, 100, 128, 129, 600, 1000, 2048, 4096, 9001, 16384):
+        rising([(m, tte.tt_emb_norm_workspace_bytes(BF16, m, dim)) for m in range(0, 9000)])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt,most,fewer,dim,hidden", [
     (BF16, 2049, (2048, 1500, 40, 3), 4096, 1024), (F16, 1100, (1024, 500, 20), 1024, 1024),
@@ -49,6 +62,32 @@ def test_gate_in_a_larger_batchs_workspace(dt, most, fewer, dim, hidden):
             tte.tt_emb_gate_forward(x[:m], wg, wu, out, g, u, workspace=ws)
             tte.tt_emb_gate_backward(x[:m], wg, wu, g, u, d[:m], dx, dwg, dwu, workspace=ws)
             outs.append((out, g, u, dx, dwg, dwu))
+        for a, b in zip(*outs):
+            assert torch.equal(a, b)
+        assert bool((room[size:] == 77).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, F16], ids=["f32", "f16"])
+@pytest.mark.parametrize("most,fewer,classes", [(1024, (1014, 700, 341, 9, 1), 16384), (300, (256, 255, 40), 50021)])
+def test_distill_in_a_larger_batchs_workspace(dt, most, fewer, classes):
+    """The same of every form of distillation."""
+    from tests.test_dense_gpu import rand, teacher
+    size = tte.tt_emb_distill_workspace_bytes(dt, most, classes)
+    room = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda:0")
+    ids, tl, w = teacher(most, classes, 5, seed=1)
+    z = rand(most, classes, seed=2, dt=dt)
+    for m in (most, *fewer):
+        print("distill workspace", dt, m, classes, flush=True)
+        outs = []
+        for ws in (room[:size], None):
+            loss, loss2, stats = (torch.empty(*s, device="cuda:0") for s in ((m,), (m,), (m, 2)))
+            dz, dz2 = torch.empty_like(z[:m]), torch.empty_like(z[:m])
+            rows = z[:m], ids[:m], tl[:m]
+            tte.tt_emb_distill_forward(*rows, loss, stats, temperature=2.0, workspace=ws)
+            tte.tt_emb_distill_backward(*rows, stats, w[:m], dz, temperature=2.0)
+            tte.tt_emb_distill_train(*rows, w[:m], loss2, dz2, temperature=2.0, workspace=ws)
+            outs.append((loss, stats, dz, loss2, dz2))
         for a, b in zip(*outs):
             assert torch.equal(a, b)
         assert bool((room[size:] == 77).all())
