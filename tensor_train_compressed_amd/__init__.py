@@ -248,10 +248,14 @@ def core_extents(tables_c) -> tuple:
     return tuple(ext)
 
 
+def _torch_c():
+    return (sys.modules.get("torch") or __import__("torch"))._C
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         # the handle of torch.cuda.current_stream(), without making a Stream object (2.8 us a call)
-        c = sys.modules["torch"]._C
+        c = _torch_c()
         return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
@@ -580,6 +584,22 @@ def _workspace(workspace, bytes_call, sizes, what: str, like, stream):
     return workspace, _dev_ptr(workspace, "uint8", "workspace"), int(workspace.numel())
 
 
+def _launch(name: str, like, stream, *args):
+    """The call of that name on the device of `like`, on `stream` or on that device's
+    current stream (the one _workspace allocates for)."""
+    c, device = _torch_c(), like.get_device()
+    if stream is None:
+        handle = c._cuda_getCurrentRawStream(device)
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    call = getattr(load_library(), name)
+    if device == c._cuda_getDevice():
+        return _check(call(*args, handle), name)
+    import torch
+    with torch.cuda.device(device):   # a default stream's handle means the current device's
+        return _check(call(*args, handle), name)
+
+
 def tt_emb_norm_workspace_bytes(dtype, rows: int, dim: int) -> int:
     return int(load_library().tt_emb_norm_workspace_bytes(_dtype_code(dtype, "dtype"), rows, dim))
 
@@ -593,10 +613,10 @@ def tt_emb_norm_forward(x, weight, bias, y, mean=None, rstd=None, eps: float = 1
     py, ldy = _matrix(y, x.dtype, "y", rows, dim)
     _pair(mean, rstd, "mean and rstd")
     wname = _name(weight.dtype)
-    _check(load_library().tt_emb_norm_forward(
+    _launch(
+        "tt_emb_norm_forward", x, stream,
         code, wcode, px, ldx, _dev_ptr(weight, wname, "weight", dim), _dev_ptr(bias, wname, "bias", dim), py, ldy,
-        _dev_ptr(mean, "float32", "mean", rows), _dev_ptr(rstd, "float32", "rstd", rows), rows, dim, float(eps),
-        _stream(stream)), "tt_emb_norm_forward")
+        _dev_ptr(mean, "float32", "mean", rows), _dev_ptr(rstd, "float32", "rstd", rows), rows, dim, float(eps))
 
 
 def tt_emb_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias=None, workspace=None, stream=None):
@@ -609,10 +629,11 @@ def tt_emb_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias=None, wor
     wname = _name(weight.dtype)
     ws, pws, nws = _workspace(workspace, tt_emb_norm_workspace_bytes, (x.dtype, rows, dim), "tt_emb_norm_backward",
                               x, stream)
-    _check(load_library().tt_emb_norm_backward(
+    _launch(
+        "tt_emb_norm_backward", x, stream,
         code, wcode, px, ldx, _dev_ptr(weight, wname, "weight", dim), _dev_ptr(mean, "float32", "mean", rows),
         _dev_ptr(rstd, "float32", "rstd", rows), pdy, lddy, pdx, lddx, _dev_ptr(dweight, wname, "dweight", dim),
-        _dev_ptr(dbias, wname, "dbias", dim), rows, dim, pws, nws, _stream(stream)), "tt_emb_norm_backward")
+        _dev_ptr(dbias, wname, "dbias", dim), rows, dim, pws, nws)
 
 
 def tt_emb_gate_workspace_bytes(dtype, rows: int, dim: int, hidden: int) -> int:
@@ -641,10 +662,10 @@ def tt_emb_gate_forward(x, w_gate, w_up, out, gate=None, up=None, act: str = "si
     _pair(gate, up, "gate and up")
     ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes, (x.dtype, rows, dim, hidden),
                               "tt_emb_gate_forward", x, stream)
-    _check(load_library().tt_emb_gate_forward(
+    _launch(
+        "tt_emb_gate_forward", x, stream,
         code, px, ldx, pg, pu, po, ldo, _dev_ptr(gate, "float32", "gate", rows * hidden),
-        _dev_ptr(up, "float32", "up", rows * hidden), rows, dim, hidden, _ACTS[act], pws, nws, _stream(stream)),
-        "tt_emb_gate_forward")
+        _dev_ptr(up, "float32", "up", rows * hidden), rows, dim, hidden, _ACTS[act], pws, nws)
 
 
 def tt_emb_gate_backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, act: str = "silu", workspace=None,
@@ -656,11 +677,12 @@ def tt_emb_gate_backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, ac
     name = _name(x.dtype)
     ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes, (x.dtype, rows, dim, hidden),
                               "tt_emb_gate_backward", x, stream)
-    _check(load_library().tt_emb_gate_backward(
+    _launch(
+        "tt_emb_gate_backward", x, stream,
         code, px, ldx, pg, pu, _dev_ptr(gate, "float32", "gate", rows * hidden),
         _dev_ptr(up, "float32", "up", rows * hidden), pd, ldd, pdx, lddx,
         _dev_ptr(dw_gate, name, "dw_gate", hidden * dim), _dev_ptr(dw_up, name, "dw_up", hidden * dim), rows, dim,
-        hidden, _ACTS[act], pws, nws, _stream(stream)), "tt_emb_gate_backward")
+        hidden, _ACTS[act], pws, nws)
 
 
 def tt_emb_distill_workspace_bytes(dtype, rows: int, classes: int) -> int:
@@ -686,10 +708,10 @@ def tt_emb_distill_forward(logits, ids, top_logits, loss, stats=None, temperatur
     code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
     ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes, (logits.dtype, rows, classes),
                               "tt_emb_distill_forward", logits, stream)
-    _check(load_library().tt_emb_distill_forward(
+    _launch(
+        "tt_emb_distill_forward", logits, stream,
         code, pz, ld, pi, pt, top, _dev_ptr(loss, "float32", "loss", rows),
-        _dev_ptr(stats, "float32", "stats", rows * 2), rows, classes, float(temperature), pws, nws,
-        _stream(stream)), "tt_emb_distill_forward")
+        _dev_ptr(stats, "float32", "stats", rows * 2), rows, classes, float(temperature), pws, nws)
 
 
 def tt_emb_distill_backward(logits, ids, top_logits, stats, row_weight, dlogits, temperature: float = 1.0,
@@ -698,10 +720,10 @@ def tt_emb_distill_backward(logits, ids, top_logits, stats, row_weight, dlogits,
     forward kept."""
     code, pz, ld, pi, pt, top, rows, classes = _distill_sizes(logits, ids, top_logits)
     pd, ldd = _matrix(dlogits, logits.dtype, "dlogits", rows, classes)
-    _check(load_library().tt_emb_distill_backward(
+    _launch(
+        "tt_emb_distill_backward", logits, stream,
         code, pz, ld, pi, pt, top, _dev_ptr(stats, "float32", "stats", rows * 2),
-        _dev_ptr(row_weight, "float32", "row_weight", rows), pd, ldd, rows, classes, float(temperature),
-        _stream(stream)), "tt_emb_distill_backward")
+        _dev_ptr(row_weight, "float32", "row_weight", rows), pd, ldd, rows, classes, float(temperature))
 
 
 def tt_emb_distill_train(logits, ids, top_logits, row_weight, loss, dlogits, temperature: float = 1.0,
@@ -711,7 +733,7 @@ def tt_emb_distill_train(logits, ids, top_logits, row_weight, loss, dlogits, tem
     pd, ldd = _matrix(dlogits, logits.dtype, "dlogits", rows, classes)
     ws, pws, nws = _workspace(workspace, tt_emb_distill_workspace_bytes, (logits.dtype, rows, classes),
                               "tt_emb_distill_train", logits, stream)
-    _check(load_library().tt_emb_distill_train(
+    _launch(
+        "tt_emb_distill_train", logits, stream,
         code, pz, ld, pi, pt, top, _dev_ptr(row_weight, "float32", "row_weight", rows),
-        _dev_ptr(loss, "float32", "loss", rows), pd, ldd, rows, classes, float(temperature), pws, nws,
-        _stream(stream)), "tt_emb_distill_train")
+        _dev_ptr(loss, "float32", "loss", rows), pd, ldd, rows, classes, float(temperature), pws, nws)
