@@ -117,6 +117,7 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_fwd(
         if (r + step < rows) fetch(r + step);   // under way while this row is reduced
         row_sum2<TPR>(s, q, sm, slot);
         float mean = s * inv_n, var = 0.f;
+        mean = fmaf(fmaf(-mean, (float)dim, s), inv_n, mean);   // s / n: a row of one value has that mean
         s = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -189,7 +190,9 @@ __global__ __launch_bounds__(norm_block<TPR>()) void k_norm_bwd(
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + t) * 8, n = dim - c;
-            nx[v] = load8n(x + r * ldx + c, n, (T)0.f);
+            // past the row's end x is its last value: its xhat is as large as the others', where
+            // that of 0 may be infinite (a row of one value, far from 0: rstd is 1/sqrt(eps))
+            nx[v] = load8n(x + r * ldx + c, n, n < 8 ? x[r * ldx + dim - 1] : (T)0.f);
             ng[v] = load8n(dy + r * lddy + c, n, (T)0.f);
         }
     };
