@@ -173,13 +173,13 @@ __global__ __launch_bounds__(256) void k_gate_grad(const float* __restrict__ gat
 struct Align {
     const void* src[3];
     void* dst[3];
-    int64_t ld[3], rows[3];
-    int cols, up, panel;   // up: cols up to a multiple of kPanel
+    int64_t ld[3], rows[3], first;   // first: of the rows of this launch
+    int cols, up, panel;             // up: cols up to a multiple of kPanel
 };
 template <class T>
 __global__ __launch_bounds__(256) void k_gate_align(const Align a) {
     const int z = blockIdx.y, quads = (a.up / kPanel + 3) / 4;
-    const int64_t r = (int64_t)(blockIdx.x / quads) * 16 + (threadIdx.x & 63) / 4;
+    const int64_t r = a.first + (int64_t)(blockIdx.x / quads) * 16 + (threadIdx.x & 63) / 4;
     const int c = (blockIdx.x % quads * 4 + threadIdx.x / 64) * kPanel + (threadIdx.x & 3) * 8;
     if (r >= a.rows[z] || c >= (a.panel == kPanel ? a.up : a.panel)) return;
     const Raw8<T> v = load8n((const T*)a.src[z] + r * a.ld[z] + c, a.cols - c, (T)0.f);
@@ -1070,10 +1070,14 @@ tt_status aligned_inputs(Inputs& in, const GateArgs& a, const GateSpace& sp, boo
             if (panels) in.pw = a.H * kPanel;
         }
         if (n == 0) return TT_OK;
-        const int64_t rows = std::max(c.rows[0], c.rows[n - 1]);
-        TT_LAUNCH(nullptr, "k_gate_align", a.s, (k_gate_align<T>),
-                  dim3((unsigned)((rows + 15) / 16 * ((sp.Kp / kPanel + 3) / 4)), n), dim3(256), 0, a.s, c);
-        TT_LAUNCH_CHECK();
+        // as many rows a launch as its threads allow, which must stay below 2^32 in all
+        const int64_t rows = std::max(c.rows[0], c.rows[n - 1]), quads = (sp.Kp / kPanel + 3) / 4;
+        const int64_t step = (int64_t(1) << 22) / quads * 16;
+        for (c.first = 0; c.first < rows; c.first += step) {
+            const int64_t groups = (std::min(step, rows - c.first) + 15) / 16 * quads;
+            TT_LAUNCH(nullptr, "k_gate_align", a.s, (k_gate_align<T>), dim3((unsigned)groups, n), dim3(256), 0, a.s, c);
+            TT_LAUNCH_CHECK();
+        }
         return TT_OK;
     }
 }
