@@ -392,9 +392,11 @@ tt_status tt_emb_norm_backward(int32_t dtype, int32_t wdtype, const void* x, int
  *   gate, up  float[rows][hidden], the projections before the activation, as
  *             the backward needs them; both NULL when serving
  * TT_F32 products are formed from three bf16 parts of each operand to fp32
- * accuracy; an infinity in an operand gives NaN. The backward's factors
+ * accuracy (operands below 2^-110 keep fewer digits: 1e-5 at 2^-120, 8e-4 at
+ * 2^-126); an infinity in an operand gives NaN. The backward's factors
  * dout * up * act'(gate) and dout * act(gate) are rounded to dtype before
- * their products, so with TT_F16 they must lie in its range.
+ * their products, so with TT_F16 they must lie in its range (past 65504 the
+ * gradients they go into are infinite or NaN).
  * Limits: dim, hidden < 2^20, rows < 2^22, row stride of x < 2^22. */
 size_t tt_emb_gate_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden);
 tt_status tt_emb_gate_forward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate, const void* w_up,

@@ -16,7 +16,8 @@
 // Types. bf16 and f16 operands go to the matrix cores as they are; dg and du
 // are rounded to them (half a step of 2^-8 or 2^-11, the size of the error that
 // the rounding of dx, dWg and dWu themselves has). fp32 operands are cut into
-// three bf16 planes, x = x0 + x1 + x2 exactly (8 digits each), and a product
+// three bf16 planes, x = x0 + x1 + x2 exactly (8 digits each; down to 2^-110,
+// where the last plane's digits end), and a product
 // is the sum of the six plane products down to 2^-16; the three left out are
 // below 2^-24 of |a||b|, the rounding of an fp32 product. Six bf16 products
 // take 6/16 of the matrix cores' time for an fp32 one. Sums are fp32 throughout.
