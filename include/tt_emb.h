@@ -399,6 +399,8 @@ tt_status tt_emb_norm_backward(int32_t dtype, int32_t wdtype, const void* x, int
  * gradients they go into are infinite or NaN).
  * Limits: dim, hidden < 2^20, rows < 2^22, row stride of x < 2^22. */
 size_t tt_emb_gate_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden);
+/* What tt_emb_gate_forward alone needs, for a program that only serves. */
+size_t tt_emb_gate_forward_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden);
 tt_status tt_emb_gate_forward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate, const void* w_up,
                               void* out, int64_t ldout, float* gate, float* up, int64_t rows, int64_t dim,
                               int64_t hidden, int32_t act, void* workspace, size_t workspace_bytes, void* stream);

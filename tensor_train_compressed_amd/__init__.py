@@ -28,7 +28,7 @@ __all__ = [
     "tt_emb_forward_cached", "tt_emb_backward_cached", "tt_emb_backward_sgd_cached", "HotCache",
     "TT_PATH_MATRIX_CORE", "TT_PATH_GENERIC", "TT_ERR_STALE", "TT_ERR_SCRATCH", "TT_ERR_CACHE", "Plan",
     "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
-    "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
+    "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
     "tt_emb_distill_backward", "tt_emb_distill_train",
     "EXPORTS",
 ]
@@ -55,7 +55,7 @@ EXPORTS = (
     "tt_emb_kernel_times", "tt_emb_cache_bytes", "tt_emb_cache_build", "tt_emb_plan_cached",
     "tt_emb_forward_cached", "tt_emb_backward_cached", "tt_emb_backward_sgd_cached", "tt_emb_status_string",
     "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
-    "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
+    "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
     "tt_emb_distill_backward", "tt_emb_distill_train",
 )
 
@@ -152,10 +152,11 @@ def load_library() -> ctypes.CDLL:
         lib.tt_emb_status_string.argtypes = [ctypes.c_int]
         lib.tt_emb_status_string.restype = ctypes.c_char_p
         sz, f32 = ctypes.c_size_t, ctypes.c_float
-        for op in ("norm", "gate", "distill"):
+        for op in ("norm", "gate", "gate_forward", "distill"):
             getattr(lib, f"tt_emb_{op}_workspace_bytes").restype = sz
         lib.tt_emb_norm_workspace_bytes.argtypes = [i32, i64, i64]
         lib.tt_emb_gate_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        lib.tt_emb_gate_forward_workspace_bytes.argtypes = [i32, i64, i64, i64]
         lib.tt_emb_distill_workspace_bytes.argtypes = [i32, i64, i64]
         lib.tt_emb_norm_forward.argtypes = [i32, i32, P, i64, P, P, P, i64, P, P, i64, i64, f32, P]
         lib.tt_emb_norm_backward.argtypes = [i32, i32, P, i64, P, P, P, P, i64, P, i64, P, P, i64, i64, P, sz, P]
@@ -640,6 +641,11 @@ def tt_emb_gate_workspace_bytes(dtype, rows: int, dim: int, hidden: int) -> int:
     return int(load_library().tt_emb_gate_workspace_bytes(_dtype_code(dtype, "dtype"), rows, dim, hidden))
 
 
+def tt_emb_gate_forward_workspace_bytes(dtype, rows: int, dim: int, hidden: int) -> int:
+    """Of a program that only serves: what tt_emb_gate_forward alone needs."""
+    return int(load_library().tt_emb_gate_forward_workspace_bytes(_dtype_code(dtype, "dtype"), rows, dim, hidden))
+
+
 def _gate_sizes(x, w_gate, w_up, act):
     if act not in _ACTS:
         raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
@@ -660,7 +666,7 @@ def tt_emb_gate_forward(x, w_gate, w_up, out, gate=None, up=None, act: str = "si
     code, px, ldx, pg, pu, rows, dim, hidden = _gate_sizes(x, w_gate, w_up, act)
     po, ldo = _matrix(out, x.dtype, "out", rows, hidden)
     _pair(gate, up, "gate and up")
-    ws, pws, nws = _workspace(workspace, tt_emb_gate_workspace_bytes, (x.dtype, rows, dim, hidden),
+    ws, pws, nws = _workspace(workspace, tt_emb_gate_forward_workspace_bytes, (x.dtype, rows, dim, hidden),
                               "tt_emb_gate_forward", x, stream)
     _launch(
         "tt_emb_gate_forward", x, stream,

@@ -929,13 +929,13 @@ size_t partial_bytes(int32_t dtype, const Sum (&p)[N]) {
 
 // Where things lie in the workspace (bytes): x and the weights with aligned
 // rows (16-bit types; used where the caller's are not), the backward's dg and
-// du, partial sums. forward, backward: what a call of these sizes needs; most:
-// what one of these sizes or of fewer rows does (splits come and go with the rows,
-// all else only grows).
+// du, partial sums. forward, backward: what a call of these sizes needs;
+// most_forward, most: what a forward, or either, of these sizes or of fewer rows
+// does (splits come and go with the rows, all else only grows).
 struct GateSpace {
     int64_t Kp, Hp;
     Cut fwd[1], back[2];   // back: dx, dW
-    size_t x, wg, wu, gu, part, part_dx, part_dw, forward, backward, most;
+    size_t x, wg, wu, gu, part, part_dx, part_dw, forward, backward, most_forward, most;
     GateSpace(int32_t dtype, int64_t M, int64_t K, int64_t H) : Kp(up_to(K, kPanel)), Hp(up_to(H, kPanel)) {
         const int64_t k = (K + kBK - 1) / kBK, h = (H + kBK - 1) / kBK, m = (M + kBK - 1) / kBK;
         const Sum fwd_sums[1] = {{M, 2 * H, k, 1}}, back_sums[2] = {{M, K, 2 * h, 1}, {H, K, m, 2}};
@@ -954,15 +954,18 @@ struct GateSpace {
         gu = at;
         part = gu;
         const size_t few = 256;
-        forward = std::max(few, at + (few_rows(dtype, M, K, H) || fwd[0].splits == 1
-                                          ? 0 : (size_t)fwd[0].splits * 2 * M * H * 4));
-        most = at + partial_bytes(dtype, fwd_sums);
+        if (few_rows(dtype, M, K, H)) {   // (and any smaller M)
+            forward = most_forward = few;
+        } else {
+            forward = std::max(few, at + (fwd[0].splits == 1 ? 0 : (size_t)fwd[0].splits * 2 * M * H * 4));
+            most_forward = std::max(few, at + partial_bytes(dtype, fwd_sums));
+        }
         take(M * 2 * Hp * (dtype == TT_F32 ? 4 : 2));
         const size_t parts = at;
         part_dx = take(back[0].splits == 1 ? 0 : (size_t)back[0].splits * M * K * 4);
         part_dw = take(back[1].splits == 1 ? 0 : (size_t)back[1].splits * 2 * H * K * 4);
         backward = std::max(few, at);
-        most = std::max({few, most, parts + partial_bytes(dtype, back_sums)});
+        most = std::max({few, most_forward, parts + partial_bytes(dtype, back_sums)});
     }
 };
 
@@ -1163,6 +1166,11 @@ using namespace tt;
 extern "C" size_t tt_emb_gate_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden) {
     if (gate_check(dtype, rows, dim, hidden) != TT_OK) return 0;
     return GateSpace(dtype, rows, dim, hidden).most;
+}
+
+extern "C" size_t tt_emb_gate_forward_workspace_bytes(int32_t dtype, int64_t rows, int64_t dim, int64_t hidden) {
+    if (gate_check(dtype, rows, dim, hidden) != TT_OK) return 0;
+    return GateSpace(dtype, rows, dim, hidden).most_forward;
 }
 
 extern "C" tt_status tt_emb_gate_forward(int32_t dtype, const void* x, int64_t ldx, const void* w_gate,

@@ -30,6 +30,18 @@ def test_gate_workspace_serves_fewer_rows():
             rising([(m, tte.tt_emb_gate_workspace_bytes(dt, m, dim, hidden)) for m in row_counts(rng)])
 
 
+def test_gate_forward_asks_for_its_own_workspace():
+    """A token through large weights needs none of the training step's room; no forward needs more than training."""
+    rng = random.Random(5)
+    assert tte.tt_emb_gate_forward_workspace_bytes(BF16, 1, 4096, 10240) <= 4096
+    for dim, hidden in [(4096, 1024), (4096, 10240), (512, 1536), (1, 1)]:
+        for dt in (F32, F16):
+            sizes = [(m, tte.tt_emb_gate_forward_workspace_bytes(dt, m, dim, hidden)) for m in row_counts(rng)]
+            rising(sizes)
+            assert all(s <= tte.tt_emb_gate_workspace_bytes(dt, m, dim, hidden) for m, s in sizes)
+    assert tte.load_library().tt_emb_gate_forward_workspace_bytes(1, 2, 8, 0) == 0
+
+
 def test_distill_workspace_serves_fewer_rows():
     rng = random.Random(4)
     for classes in [1, 2048, 4096, 4097, 16384, 16385, 50021, 131072, 1000000, 1 << 22] + \
@@ -64,6 +76,26 @@ def test_gate_in_a_larger_batchs_workspace(dt, most, fewer, dim, hidden):
             outs.append((out, g, u, dx, dwg, dwu))
         for a, b in zip(*outs):
             assert torch.equal(a, b)
+        assert bool((room[size:] == 77).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16, F16], ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("most,fewer,dim,hidden", [(16, (3, 1), 1030, 700), (32, (17,), 520, 700), (33, (32, 1), 4096, 4200),
+                                                   (1100, (1037, 300, 16), 1030, 700), (600, (512, 64), 4096, 1024)])
+def test_gate_forward_in_its_own_workspace(dt, most, fewer, dim, hidden):
+    from tests.test_dense_gpu import gate_inputs
+    size = tte.tt_emb_gate_forward_workspace_bytes(dt, most, dim, hidden)
+    full = torch.empty(tte.tt_emb_gate_workspace_bytes(dt, most, dim, hidden), dtype=torch.uint8, device="cuda:0")
+    room = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda:0")
+    x, wg, wu, _ = gate_inputs(most, dim, hidden, dt, train=False)
+    for m in (most, *fewer):
+        print("gate forward workspace", dt, m, dim, hidden, flush=True)
+        outs = []
+        for ws in (room[:size], full, None):
+            outs.append(torch.empty(m, hidden, dtype=dt, device="cuda:0"))
+            tte.tt_emb_gate_forward(x[:m], wg, wu, outs[-1], workspace=ws)
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
         assert bool((room[size:] == 77).all())
 
 
