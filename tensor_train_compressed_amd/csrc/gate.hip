@@ -1030,9 +1030,12 @@ tt_status backward_products(const Product& dx, const Product& dw, bool big, hipS
 // copied to the workspace where a row does not start at a whole 16-byte piece.
 // The copies are cut into panels for the forward, which reads them by rows: a
 // step's tile is then one piece of memory instead of 64 bytes a row. That alone
-// pays for copying aligned inputs too where a product is long enough for its
-// inputs: at 8192 x 4096 x 10240 bf16 (M N / (M + 2 N) = 2925) 74 us of copies save
-// 137 of 1334 us.
+// pays for copying aligned inputs too where a product is long enough beside its
+// inputs, M H / (M + 2 H) from 2700 on (bf16 forward, copied and as they are, us):
+// 8192 x 4096 x 10240 (2925) 1061 and 1122, 32768 x 1024 x 4096 (3276) 620 and 627,
+// 16384 x 512 x 16384 (5461) 865 and 951, 16384 x 1024 x 4096 (2730) 316 and 316;
+// but 6144 x 4096 x 10240 (2363) 836 and 819, 8192 x 4096 x 4096 (2048) 433 and 421,
+// 4096 x 8192 x 16384 (1820) 1688 and 1609.
 struct Inputs {
     const void *x, *wg, *wu;
     int64_t ldx, px, ldw, pw;   // from line to line, from panel to panel
@@ -1043,7 +1046,7 @@ tt_status aligned_inputs(Inputs& in, const GateArgs& a, const GateSpace& sp, boo
     if constexpr (sizeof(T) == 4) {
         return TT_OK;
     } else {
-        const bool pays = panels && a.M * a.H / (a.M + 2 * a.H) >= 2000;
+        const bool pays = panels && a.M * a.H / (a.M + 2 * a.H) >= 2700;
         const bool x = pays || a.K % 8 != 0 || a.ldx % 8 != 0 || ((uintptr_t)a.x & 15) != 0;
         const bool w = pays || a.K % 8 != 0 || (((uintptr_t)a.wg | (uintptr_t)a.wu) & 15) != 0;
         Align c{};
