@@ -28,8 +28,8 @@ __all__ = [
     "tt_emb_forward_cached", "tt_emb_backward_cached", "tt_emb_backward_sgd_cached", "HotCache",
     "TT_PATH_MATRIX_CORE", "TT_PATH_GENERIC", "TT_ERR_STALE", "TT_ERR_SCRATCH", "TT_ERR_CACHE", "Plan",
     "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
-    "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
-    "tt_emb_distill_backward", "tt_emb_distill_train",
+    "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward",
+    "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train",
     "EXPORTS",
 ]
 
@@ -55,8 +55,8 @@ EXPORTS = (
     "tt_emb_kernel_times", "tt_emb_cache_bytes", "tt_emb_cache_build", "tt_emb_plan_cached",
     "tt_emb_forward_cached", "tt_emb_backward_cached", "tt_emb_backward_sgd_cached", "tt_emb_status_string",
     "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
-    "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward", "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward",
-    "tt_emb_distill_backward", "tt_emb_distill_train",
+    "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward",
+    "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
