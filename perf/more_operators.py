@@ -1,0 +1,508 @@
+"""Timed cases of the attention operators that train and serve a layer on
+looked-up rows: norms of queries and keys with the position rotation, attention
+over packed whole prompts, and attention of one new token over a paged cache.
+
+run() computes them in their plain form (elementary torch operations in 32
+bits, rounded once at the end; the rotation's angles in 64) while `own` is
+false, and through the library's public calls when it is true. Sizes are this
+repository's own (histories of about 20 lookups as its bags are, rows of 128
+elements in heads of 32, radix-like odd counts) or generic model widths.
+"""
+import math
+
+import torch
+
+own = False   # set from outside: false, the plain forms; true, the library's calls
+
+DEV = "cuda:0"
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+EPS = 1e-6
+BASE = 10000.0   # of the rotation's frequencies
+
+# --------------------------------------------------------------------------
+# Cases. `mode`: "forward" is the serving form; "train" is the training step of
+# the operator (forward and every gradient); "append" is the rotation of new
+# tokens whose keys and values go into the paged cache. `lengths`: "one" is a
+# single sequence of all rows, "ragged" sequences of unlike lengths, "bags"
+# histories of 1 to 100 lookups, 20 on average.
+
+
+def listed():
+    return [
+        # the newest token of one conversation, its key and value into the cache: latency
+        {"name": "rotate-append-token", "op": "rotate", "mode": "append", "dtype": "bf16", "wdtype": "f32", "rows": 1,
+         "heads": 32, "kv_heads": 8, "dim": 128, "rot": 128, "pairs": "halves", "pad": 0, "page": 16},
+        # a training batch of a wide model
+        {"name": "rotate-wide-train", "op": "rotate", "mode": "train", "dtype": "bf16", "wdtype": "f32", "rows": 8192,
+         "heads": 32, "kv_heads": 8, "dim": 128, "rot": 128, "pairs": "halves", "pad": 0, "page": 0},
+        # ragged: odd counts, a part of each head rotated, rows out of a wider buffer
+        {"name": "rotate-odd-train", "op": "rotate", "mode": "train", "dtype": "f16", "wdtype": "f16", "rows": 1021,
+         "heads": 10, "kv_heads": 5, "dim": 80, "rot": 20, "pairs": "neighbours", "pad": 3, "page": 0},
+        # a few histories of looked-up rows, answered: latency
+        {"name": "attend-answer", "op": "attend", "mode": "forward", "dtype": "f32", "rows": 320, "lengths": "bags",
+         "tail": 0, "heads": 4, "kv_heads": 4, "dim": 32, "causal": True, "pad": 0},
+        # a batch of histories at the table's dim, fp32, trained
+        {"name": "attend-histories-train", "op": "attend", "mode": "train", "dtype": "f32", "rows": 8192,
+         "lengths": "bags", "tail": 0, "heads": 4, "kv_heads": 4, "dim": 32, "causal": True, "pad": 0},
+        # one long prompt of a wide model, trained: the largest
+        {"name": "attend-long-train", "op": "attend", "mode": "train", "dtype": "bf16", "rows": 8192, "lengths": "one",
+         "tail": 0, "heads": 32, "kv_heads": 8, "dim": 128, "causal": True, "pad": 0},
+        # prompts of unlike lengths packed together, small heads, trained
+        {"name": "attend-packed-train", "op": "attend", "mode": "train", "dtype": "bf16", "rows": 8192,
+         "lengths": "ragged", "tail": 0, "heads": 16, "kv_heads": 2, "dim": 64, "causal": True, "pad": 0},
+        # ragged: no size a multiple of a tile, both directions, rows behind the last sequence
+        {"name": "attend-odd", "op": "attend", "mode": "forward", "dtype": "f16", "rows": 2731, "lengths": "ragged",
+         "tail": 13, "heads": 6, "kv_heads": 3, "dim": 72, "causal": False, "pad": 5},
+        # one new token of one long conversation: the cache is read once
+        {"name": "paged-token", "op": "paged", "mode": "forward", "dtype": "bf16", "seqs": 1, "most": 32768,
+         "fill": 1.0, "heads": 32, "kv_heads": 8, "dim": 128, "page": 16},
+        # a serving batch of conversations of unlike lengths
+        {"name": "paged-batch", "op": "paged", "mode": "forward", "dtype": "bf16", "seqs": 64, "most": 16384,
+         "fill": 0.5, "heads": 32, "kv_heads": 8, "dim": 128, "page": 16},
+        # ragged: odd counts, large odd pages, some sequences not begun
+        {"name": "paged-odd", "op": "paged", "mode": "forward", "dtype": "f16", "seqs": 17, "most": 5003,
+         "fill": 0.5, "heads": 10, "kv_heads": 5, "dim": 80, "page": 49},
+        # histories at the table's dim, fp32
+        {"name": "paged-histories", "op": "paged", "mode": "forward", "dtype": "f32", "seqs": 256, "most": 100,
+         "fill": 0.2, "heads": 4, "kv_heads": 4, "dim": 32, "page": 64},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _size(rng, lo, hi):
+    """A size of [lo, hi]: half of them odd, the others 4 or 5 times a power of two."""
+    n = _log_int(rng, lo, hi)
+    if n < 64 or rng.random() < 0.5:
+        return min(hi, n | 1)
+    unit = 1 << (n.bit_length() - 3)
+    return max(lo, (5 if n >= 5 * unit else 4) * unit)
+
+
+def draw(rng):
+    op = rng.choice(["rotate", "attend", "paged"])
+    own_kind = [work(c) for c in listed() if c["op"] == op]
+    most = {k: max(w[k] for w in own_kind) for k in ("bytes", "flops")}
+    while True:
+        kv = rng.choice([1, 2, 3, 4, 5, 8])
+        heads = kv * rng.choice([1, 1, 2, 4, 4, 7, 8])
+        dim = rng.choice([16, 32, 33, 40, 64, 64, 72, 80, 96, 101, 112, 128, 128, 128])
+        dtype = rng.choice(["f32", "bf16", "bf16", "f16"])
+        pad = rng.choice([0, 0, 0, 1, 8, 24])
+        c = {"op": op, "mode": "forward", "dtype": dtype, "heads": heads, "kv_heads": kv, "dim": dim}
+        if heads > 32:
+            continue
+        if op == "rotate":
+            rot = 2 * rng.randint(1, dim // 2) if rng.random() < 0.4 else dim // 2 * 2
+            c.update(mode=rng.choice(["forward", "append", "train"]), wdtype=rng.choice(["f32", dtype]),
+                     rows=_size(rng, 1, 16384), rot=rot, pairs=rng.choice(["halves", "neighbours"]), pad=pad, page=rng.choice([1, 16, 49, 64, 256]))
+        elif op == "attend":
+            mode = rng.choice(["forward", "train"])
+            # (a row that sees itself alone has no gradient in its query and key)
+            c.update(mode=mode, rows=_size(rng, 64 if mode == "train" else 1, 8192),
+                     lengths=rng.choice(["one", "ragged", "bags"]), tail=rng.choice([0, 0, 1, 30]), causal=rng.random() < 0.75, pad=pad)
+            c["tail"] = min(c["tail"], c["rows"] // 2)
+        else:
+            c.update(seqs=_log_int(rng, 1, 256), most=_size(rng, 1, 131072), fill=rng.choice([0.2, 0.5, 1.0]),
+                     page=rng.choice([1, 16, 16, 32, 49, 64, 256]))
+        w = work(c)
+        pages = c.get("seqs", 0) * c.get("most", 0) * kv * dim * 2 * DTYPES[dtype].itemsize
+        if w["bytes"] <= most["bytes"] and w["flops"] <= most["flops"] and pages <= 4.5e9:
+            return c
+
+
+def _lengths(c):
+    """The sequences' lengths of an "attend" case (`tail` rows lie behind the last); by the case alone."""
+    n = c["rows"] - c["tail"]
+    if c["lengths"] == "one":
+        return [n]
+    out, i = [], 0
+    if c["lengths"] == "bags":        # 1 to 100, 20 on average, as the table's bags are
+        while n > 0:
+            out.append(min(n, (17, 24, 3, 21, 19, 31, 1, 22, 100, 9, 20, 14, 0, 25, 12, 8)[i % 16]))
+            n -= out[-1]
+            i += 1
+        return out
+    share = (0.31, 0.02, 0.17, 0.0, 0.23, 0.005, 0.12)
+    out = [int(s * n) for s in share]
+    return out + [n - sum(out)]
+
+
+def _cached(c):
+    """The sequences' lengths of a "paged" case: about `fill` of the most; one in eight is not begun."""
+    if c["seqs"] == 1:
+        return [max(1, c["most"])]
+    out = []
+    for i in range(c["seqs"]):
+        part = c["fill"] + min(c["fill"], 1 - c["fill"]) * (2 * ((i * 0.6180339887) % 1.0) - 1)
+        out.append(0 if i % 8 == 5 and i < c["seqs"] - 1 else min(c["most"], max(1, int(part * c["most"]))))
+    return out
+
+
+def work(case):
+    c = case
+    e = DTYPES[c["dtype"]].itemsize
+    hq, hk, d = c["heads"], c["kv_heads"], c["dim"]
+    if c["op"] == "rotate":
+        m, ws = c["rows"], DTYPES[c["wdtype"]].itemsize
+        x = m * (hq + hk) * d
+        if c["mode"] == "forward":      # queries and keys in and out; positions and weights in
+            return {"bytes": 2 * x * e + 8 * m + 2 * d * ws, "flops": 10 * x}
+        if c["mode"] == "append":       # the values too, and a slot a row
+            return {"bytes": 2 * (x + m * hk * d) * e + 16 * m + 2 * d * ws, "flops": 10 * x}
+        # also both gradients in and out, and the weights' out
+        return {"bytes": 4 * x * e + 8 * m + 4 * d * ws, "flops": 30 * x}
+    if c["op"] == "attend":
+        lens = _lengths(c)
+        n = sum(lens)
+        pairs = sum(x * (x + 1) // 2 if c["causal"] else x * x for x in lens)
+        if c["mode"] == "forward":      # queries, keys and values in, out out; two products
+            return {"bytes": (2 * hq + 2 * hk) * n * d * e + 8 * (len(lens) + 1), "flops": 4 * d * hq * pairs}
+        # also the gradient in and three out; five more products
+        return {"bytes": (4 * hq + 4 * hk) * n * d * e + 8 * (len(lens) + 1), "flops": 14 * d * hq * pairs}
+    lens = _cached(c)
+    n = sum(lens)
+    table = sum((x + c["page"] - 1) // c["page"] for x in lens) * 4
+    # keys and values of the begun sequences once, queries in, out out
+    return {"bytes": 2 * n * hk * d * e + 2 * len(lens) * hq * d * e + table + 8 * len(lens), "flops": 4 * d * hq * n}
+
+
+# --------------------------------------------------------------------------
+# Inputs.
+
+
+def _inputs(case, seed):
+    c = case
+    dt = DTYPES[c["dtype"]]
+    g = torch.Generator(device=DEV).manual_seed(seed * 2654435761 % (1 << 31) + 29)
+    hq, hk, d = c["heads"], c["kv_heads"], c["dim"]
+
+    def normal(*shape, scale=1.0, to=dt):
+        out = torch.empty(shape, dtype=to, device=DEV)
+        flat, step = out.view(-1), 1 << 27
+        for a in range(0, flat.numel(), step):
+            part = flat[a:a + step]
+            part.copy_(torch.randn(part.numel(), generator=g, device=DEV) * scale)
+        return out
+
+    if c["op"] == "paged":
+        lens = _cached(c)
+        wide = max(1, (c["most"] + c["page"] - 1) // c["page"])
+        used = [(x + c["page"] - 1) // c["page"] for x in lens]
+        pages = sum(used) + 3                       # a few belong to nobody
+        order = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+        table = torch.full((c["seqs"], wide), -1, dtype=torch.int32, device=DEV)   # -1: not yet given
+        at = 0
+        for i, u in enumerate(used):
+            table[i, :u] = order[at:at + u]
+            at += u
+        return {"q": normal(c["seqs"], hq * d, scale=1.5), "k_pages": normal(pages, c["page"], hk, d),
+                "v_pages": normal(pages, c["page"], hk, d), "table": table,
+                "lengths": torch.tensor(lens, dtype=torch.int64, device=DEV)}
+    m = c["rows"]
+    # one projection's output holds queries, keys and values of a row side by side
+    qkv = normal(m, (hq + 2 * hk) * d + c["pad"], scale=1.2)
+    s = {"q": qkv[:, :hq * d], "k": qkv[:, hq * d:(hq + hk) * d], "v": qkv[:, (hq + hk) * d:(hq + 2 * hk) * d]}
+    if c["op"] == "attend":
+        ends = torch.tensor([0] + _lengths(c), dtype=torch.int64, device=DEV)
+        s["offsets"] = torch.cumsum(ends, 0)
+        if c["mode"] == "train":
+            s["dout"] = normal(m, hq * d)
+        return s
+    wdt = DTYPES[c["wdtype"]]
+    s["q_weight"] = (1 + normal(d, scale=0.1, to=torch.float32)).to(wdt)
+    s["k_weight"] = (1 + normal(d, scale=0.1, to=torch.float32)).to(wdt)
+    # a prompt that goes on from somewhere within a long conversation
+    start = int(torch.randint(0, 100000, (1,), generator=g, device=DEV))
+    s["positions"] = start + torch.arange(m, dtype=torch.int64, device=DEV)
+    half = c["rot"] // 2
+    s["freq"] = BASE ** (-torch.arange(half, dtype=torch.float64, device=DEV) / half)
+    if c["mode"] == "append":
+        pages = (m + c["page"] - 1) // c["page"] + 2
+        s["slots"] = torch.randperm(pages * c["page"], generator=g, device=DEV)[:m]
+        if m > 8:
+            s["slots"][m // 2] = -1                 # a padded row: kept nowhere
+        s["k_pages"] = normal(pages, c["page"], hk, d)
+        s["v_pages"] = normal(pages, c["page"], hk, d)
+    if c["mode"] == "train":
+        s["dq_out"], s["dk_out"] = normal(m, hq * d), normal(m, hk * d)
+    return s
+
+
+def prepare(case, seed):
+    c = case
+    s = _inputs(case, seed)
+    s["case"] = c
+    if not own:
+        return s
+    import tensor_train_compressed_amd as tte
+    s["tte"] = tte
+    hq, hk, d = c["heads"], c["kv_heads"], c["dim"]
+    dt = s["q"].dtype
+    # the caller-owned outputs, kept statistics and workspaces of a program's loop
+    if c["op"] == "paged":
+        s["out"] = torch.empty(c["seqs"], hq * d, dtype=dt, device=DEV)
+        need = tte.tt_emb_attend_paged_workspace_bytes(dt, c["seqs"], hq, hk, d)
+        s["workspace"] = torch.empty(need, dtype=torch.uint8, device=DEV)
+        return s
+    m = c["rows"]
+    if c["op"] == "attend":
+        s["out"] = torch.zeros(m, hq * d, dtype=dt, device=DEV)     # rows behind the last sequence stay
+        if c["mode"] == "train":
+            s["lse"] = torch.empty(hq, m, dtype=torch.float32, device=DEV)
+            dqkv = torch.zeros(m, (hq + 2 * hk) * d + c["pad"], dtype=dt, device=DEV)
+            s["dq"], s["dk"] = dqkv[:, :hq * d], dqkv[:, hq * d:(hq + hk) * d]
+            s["dv"] = dqkv[:, (hq + hk) * d:(hq + 2 * hk) * d]
+            need = tte.tt_emb_attend_workspace_bytes(dt, m, hq, hk, d)
+            s["workspace"] = torch.empty(need, dtype=torch.uint8, device=DEV)
+        return s
+    s["q_out"] = torch.empty(m, hq * d, dtype=dt, device=DEV)
+    if c["mode"] != "append":
+        s["k_out"] = torch.empty(m, hk * d, dtype=dt, device=DEV)
+    if c["mode"] == "train":
+        s["dq"], s["dk"] = torch.empty_like(s["q_out"]), torch.empty_like(s["k_out"])
+        s["dq_weight"], s["dk_weight"] = torch.empty_like(s["q_weight"]), torch.empty_like(s["k_weight"])
+        need = tte.tt_emb_rotate_workspace_bytes(dt, m, hq, hk, d)
+        s["workspace"] = torch.empty(need, dtype=torch.uint8, device=DEV)
+    return s
+
+
+# --------------------------------------------------------------------------
+# One pass.
+
+
+def run(state):
+    c = state["case"]
+    return (_OWN if own else _PLAIN)[c["op"]](state, c)
+
+
+def _own_rotate(s, c):
+    tte = s["tte"]
+    how = dict(pairs=c["pairs"], eps=EPS)
+    if c["mode"] == "append":
+        tte.tt_emb_rotate_append(s["q"], s["k"], s["v"], s["q_weight"], s["k_weight"], s["positions"], s["freq"],
+                                 s["slots"], s["q_out"], s["k_pages"], s["v_pages"], **how)
+        return [s["q_out"], s["k_pages"], s["v_pages"]]
+    tte.tt_emb_rotate_forward(s["q"], s["k"], s["q_weight"], s["k_weight"], s["positions"], s["freq"], s["q_out"],
+                              s["k_out"], **how)
+    if c["mode"] == "forward":
+        return [s["q_out"], s["k_out"]]
+    tte.tt_emb_rotate_backward(s["q"], s["k"], s["q_weight"], s["k_weight"], s["positions"], s["freq"], s["dq_out"],
+                               s["dk_out"], s["dq"], s["dk"], s["dq_weight"], s["dk_weight"], workspace=s["workspace"],
+                               **how)
+    return [s[k] for k in ("q_out", "k_out", "dq", "dk", "dq_weight", "dk_weight")]
+
+
+def _own_attend(s, c):
+    tte = s["tte"]
+    heads = dict(heads=c["heads"], kv_heads=c["kv_heads"], causal=c["causal"])
+    if c["mode"] == "forward":
+        tte.tt_emb_attend_forward(s["q"], s["k"], s["v"], s["offsets"], s["out"], **heads)
+        return s["out"]
+    tte.tt_emb_attend_forward(s["q"], s["k"], s["v"], s["offsets"], s["out"], s["lse"], **heads)
+    tte.tt_emb_attend_backward(s["q"], s["k"], s["v"], s["offsets"], s["out"], s["lse"], s["dout"], s["dq"], s["dk"],
+                               s["dv"], workspace=s["workspace"], **heads)
+    return [s[k] for k in ("out", "dq", "dk", "dv")]
+
+
+def _own_paged(s, c):
+    s["tte"].tt_emb_attend_paged(s["q"], s["k_pages"], s["v_pages"], s["table"], s["lengths"], s["out"],
+                                 workspace=s["workspace"])
+    return s["out"]
+
+
+def _turns(s):
+    """Cosines and sines [rows, 1, rot / 2] of the rotation's angles, formed in 64 bits."""
+    angle = s["positions"].double()[:, None, None] * s["freq"]
+    return torch.cos(angle).float(), torch.sin(angle).float()
+
+
+def _turn(x, cos, sin, pairs):
+    """Each head's leading 2 * cos.shape[-1] elements rotated, pair by pair."""
+    half = cos.shape[-1]
+    if pairs == "halves":
+        a, b, rest = x[..., :half], x[..., half:2 * half], x[..., 2 * half:]
+        return torch.cat((a * cos - b * sin, a * sin + b * cos, rest), -1)
+    a, b, rest = x[..., 0:2 * half:2], x[..., 1:2 * half:2], x[..., 2 * half:]
+    return torch.cat((torch.stack((a * cos - b * sin, a * sin + b * cos), -1).flatten(-2), rest), -1)
+
+
+def _plain_norms(x, w, c):
+    n = x.float().unflatten(1, (-1, c["dim"]))
+    r = 1.0 / torch.sqrt((n * n).sum(-1, keepdim=True) / c["dim"] + EPS)
+    return n * r, r, w.float()
+
+
+def _plain_back(x, w, dy, cos, sin, c):
+    n, r, w32 = _plain_norms(x, w, c)
+    g = _turn(dy.float().unflatten(1, (-1, c["dim"])), cos, -sin, c["pairs"])
+    t = g * w32
+    dx = r * (t - n * ((t * n).sum(-1, keepdim=True) / c["dim"]))
+    return dx.flatten(1).to(x.dtype), (g * n).sum((0, 1)).to(w.dtype)
+
+
+def _plain_rotate(s, c):
+    cos, sin = _turns(s)
+    dt = s["q"].dtype
+    n, _, w = _plain_norms(s["q"], s["q_weight"], c)
+    q_out = _turn(n * w, cos, sin, c["pairs"]).flatten(1).to(dt)
+    n, _, w = _plain_norms(s["k"], s["k_weight"], c)
+    k_out = _turn(n * w, cos, sin, c["pairs"]).flatten(1).to(dt)
+    if c["mode"] == "forward":
+        return [q_out, k_out]
+    if c["mode"] == "append":
+        width = c["kv_heads"] * c["dim"]
+        keep = s["slots"] >= 0
+        # a row without a slot writes what its neighbour in the list of slots writes
+        src = torch.where(keep, torch.arange(c["rows"], device=DEV), 0)
+        slots = s["slots"][src]
+        s["k_pages"].view(-1, width)[slots] = k_out[src]
+        s["v_pages"].view(-1, width)[slots] = s["v"][src]
+        return [q_out, s["k_pages"], s["v_pages"]]
+    dq, dwq = _plain_back(s["q"], s["q_weight"], s["dq_out"], cos, sin, c)
+    dk, dwk = _plain_back(s["k"], s["k_weight"], s["dk_out"], cos, sin, c)
+    return [q_out, k_out, dq, dk, dwq, dwk]
+
+
+def _grouped(x, kv_heads, dim):
+    """[rows, heads * dim] as float32 [kv_heads, heads of the group * rows, dim]."""
+    x = x.float().view(x.shape[0], kv_heads, -1, dim)
+    return x.permute(1, 2, 0, 3).reshape(kv_heads, -1, dim)
+
+
+def _rows_of(x, rows):
+    """Back from _grouped."""
+    kv, _, dim = x.shape
+    return x.view(kv, -1, rows, dim).permute(2, 0, 1, 3).reshape(rows, -1)
+
+
+def _plain_attend(s, c):
+    m, hk, d, dt = c["rows"], c["kv_heads"], c["dim"], s["q"].dtype
+    scale = 1.0 / math.sqrt(d)
+    row = torch.arange(m, device=DEV)
+    seq = torch.bucketize(row, s["offsets"], right=True)      # past the last: of no sequence
+    there = row < s["offsets"][-1]
+    near = (seq[:, None] == seq[None, :]) & there[:, None] & there[None, :]
+    if c["causal"]:
+        near = near & (row[:, None] >= row[None, :])
+    q, k, v = _grouped(s["q"], hk, d), _grouped(s["k"], hk, d), _grouped(s["v"], hk, d)
+    p = torch.matmul(q, k.transpose(1, 2)).view(hk, -1, m, m)
+    p = torch.where(near, p * scale, float("-inf"))
+    top = p.max(-1, keepdim=True).values
+    p = torch.exp(p - torch.where(top == float("-inf"), 0.0, top))
+    total = p.sum(-1, keepdim=True)
+    p = (p / torch.where(total == 0.0, 1.0, total)).view(hk, -1, m)
+    out = torch.matmul(p, v)
+    answer = _rows_of(out, m).to(dt)
+    if c["mode"] == "forward":
+        return answer
+    do = _grouped(s["dout"], hk, d)
+    dv = torch.matmul(p.transpose(1, 2), do)
+    ds = torch.matmul(do, v.transpose(1, 2)) - (do * out).sum(-1, keepdim=True)
+    ds = ds * p * scale
+    dq, dk = torch.matmul(ds, k), torch.matmul(ds.transpose(1, 2), q)
+    return [answer, _rows_of(dq, m).to(dt), _rows_of(dk, m).to(dt), _rows_of(dv, m).to(dt)]
+
+
+def _plain_paged(s, c):
+    hk, d, n = c["kv_heads"], c["dim"], c["seqs"]
+    pages = s["table"].clamp_min(0).long()
+    k = s["k_pages"][pages].flatten(1, 2).float().permute(0, 2, 1, 3)     # [seqs, kv_heads, slots, dim]
+    v = s["v_pages"][pages].flatten(1, 2).float().permute(0, 2, 1, 3)
+    q = s["q"].float().view(n, hk, -1, d) / math.sqrt(d)
+    p = torch.matmul(q, k.transpose(2, 3))
+    there = torch.arange(p.shape[3], device=DEV) < s["lengths"][:, None, None, None]
+    p = torch.where(there, p, float("-inf"))
+    top = p.max(-1, keepdim=True).values
+    p = torch.exp(p - torch.where(top == float("-inf"), 0.0, top))
+    total = p.sum(-1, keepdim=True)
+    out = torch.matmul(p / torch.where(total == 0.0, 1.0, total), v)
+    return out.view(n, -1).to(s["q"].dtype)
+
+
+_OWN = {"rotate": _own_rotate, "attend": _own_attend, "paged": _own_paged}
+_PLAIN = {"rotate": _plain_rotate, "attend": _plain_attend, "paged": _plain_paged}
+
+
+# --------------------------------------------------------------------------
+# The same outputs in 64 bits, from the definitions and by differentiating
+# them.
+
+
+def _exact_rotated(x, w, s, c):
+    """By complex numbers: a pair times e^(i angle)."""
+    d, half = c["dim"], c["rot"] // 2
+    h = x.view(x.shape[0], -1, d)
+    u = h * torch.rsqrt((h * h).mean(-1, keepdim=True) + EPS) * w
+    turned, rest = u[..., :2 * half], u[..., 2 * half:]
+    halves = c["pairs"] == "halves"
+    pairs = turned.unflatten(-1, (2, half)).transpose(-1, -2) if halves else turned.unflatten(-1, (half, 2))
+    z = torch.view_as_complex(pairs.contiguous())
+    angle = torch.outer(s["positions"].double(), s["freq"])
+    y = torch.view_as_real(z * torch.polar(torch.ones_like(angle), angle)[:, None])
+    y = (y.transpose(-1, -2) if halves else y).flatten(-2)
+    return torch.cat((y, rest), -1).flatten(1)
+
+
+def exact(case, seed):
+    c = case
+    s = _inputs(case, seed)
+    if c["op"] == "rotate":
+        q, k, wq, wk = (s[x].double().contiguous().requires_grad_() for x in ("q", "k", "q_weight", "k_weight"))
+        yq, yk = _exact_rotated(q, wq, s, c), _exact_rotated(k, wk, s, c)
+        if c["mode"] == "forward":
+            return [yq.detach(), yk.detach()]
+        if c["mode"] == "append":
+            kp, vp = s["k_pages"].double(), s["v_pages"].double()
+            keep = s["slots"] >= 0
+            kp.flatten(2).flatten(0, 1)[s["slots"][keep]] = yk.detach()[keep]
+            vp.flatten(2).flatten(0, 1)[s["slots"][keep]] = s["v"].double()[keep]
+            return [yq.detach(), kp, vp]
+        dq, dwq = torch.autograd.grad(yq, (q, wq), s["dq_out"].double())
+        dk, dwk = torch.autograd.grad(yk, (k, wk), s["dk_out"].double())
+        return [yq.detach(), yk.detach(), dq, dk, dwq, dwk]
+    hq, hk, d = c["heads"], c["kv_heads"], c["dim"]
+    group, scale = hq // hk, d ** -0.5
+    if c["op"] == "paged":
+        out = torch.zeros(c["seqs"], hq, d, dtype=torch.float64, device=DEV)
+        for i, n in enumerate(_cached(c)):
+            if n == 0:
+                continue
+            at = torch.arange(n, device=DEV)
+            slot = s["table"][i].long()[at // c["page"]] * c["page"] + at % c["page"]
+            k = s["k_pages"].flatten(0, 1)[slot].double().transpose(0, 1)
+            v = s["v_pages"].flatten(0, 1)[slot].double().transpose(0, 1)
+            q = s["q"][i].double().view(hk, group, d)
+            out[i] = (torch.softmax(q @ k.transpose(1, 2) * scale, -1) @ v).view(hq, d)
+        return out.flatten(1)
+    m = c["rows"]
+    train = c["mode"] == "train"
+    out, dq = (torch.zeros(m, hq, d, dtype=torch.float64, device=DEV) for _ in range(2))
+    dk, dv = (torch.zeros(m, hk, d, dtype=torch.float64, device=DEV) for _ in range(2))
+    q, k, v = (s[x].reshape(m, -1, d) for x in ("q", "k", "v"))
+    do = s["dout"].view(m, hq, d) if train else None
+    at = 0
+    for n in _lengths(c):
+        rows, at = slice(at, at + n), at + n
+        if n == 0:
+            continue
+        hidden = torch.ones(n, n, dtype=torch.bool, device=DEV).triu(1) if c["causal"] else None
+        for h in range(hk) if n > 1000 else (slice(0, hk),):
+            # [kv heads, group, n, d] and [kv heads, 1, n, d]
+            qs = q[rows].unflatten(1, (hk, group))[:, h].double().reshape(n, -1, group, d).permute(1, 2, 0, 3)
+            ks, vs = (x[rows][:, h].double().reshape(n, -1, 1, d).permute(1, 2, 0, 3) for x in (k, v))
+            qs, ks, vs = (x.contiguous().requires_grad_() for x in (qs, ks, vs))
+            z = torch.matmul(qs, ks.transpose(2, 3)) * scale
+            o = torch.matmul(torch.softmax(z if hidden is None else z.masked_fill(hidden, -torch.inf), -1), vs)
+            first, last = (h, h + 1) if isinstance(h, int) else (0, hk)
+            out[rows, first * group:last * group] = o.detach().permute(2, 0, 1, 3).reshape(n, -1, d)
+            if train:
+                g = do[rows, first * group:last * group].double().view(n, -1, group, d).permute(1, 2, 0, 3)
+                for whole, part, i, j in zip((dq, dk, dv), torch.autograd.grad(o, (qs, ks, vs), g),
+                                             (first * group, first, first), (last * group, last, last)):
+                    whole[rows, i:j] = part.permute(2, 0, 1, 3).reshape(n, -1, d)
+    if not train:
+        return out.flatten(1)
+    return [x.flatten(1) for x in (out, dq, dk, dv)]
