@@ -97,12 +97,14 @@ def draw(rng):
         if op == "rotate":
             rot = 2 * rng.randint(1, dim // 2) if rng.random() < 0.4 else dim // 2 * 2
             c.update(mode=rng.choice(["forward", "append", "train"]), wdtype=rng.choice(["f32", dtype]),
-                     rows=_size(rng, 1, 16384), rot=rot, pairs=rng.choice(["halves", "neighbours"]), pad=pad, page=rng.choice([1, 16, 49, 64, 256]))
+                     rows=_size(rng, 1, 16384), rot=rot, pairs=rng.choice(["halves", "neighbours"]), pad=pad,
+                     page=rng.choice([1, 16, 49, 64, 256]))
         elif op == "attend":
             mode = rng.choice(["forward", "train"])
             # (a row that sees itself alone has no gradient in its query and key)
             c.update(mode=mode, rows=_size(rng, 64 if mode == "train" else 1, 8192),
-                     lengths=rng.choice(["one", "ragged", "bags"]), tail=rng.choice([0, 0, 1, 30]), causal=rng.random() < 0.75, pad=pad)
+                     lengths=rng.choice(["one", "ragged", "bags"]), tail=rng.choice([0, 0, 1, 30]),
+                     causal=rng.random() < 0.75, pad=pad)
             c["tail"] = min(c["tail"], c["rows"] // 2)
         else:
             c.update(seqs=_log_int(rng, 1, 256), most=_size(rng, 1, 131072), fill=rng.choice([0.2, 0.5, 1.0]),
