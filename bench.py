@@ -247,7 +247,8 @@ def hot_rows_step(args):
 
 
 # The dense operators' sources: no kernel of the measured path is in them.
-DENSE_SOURCES = ("tt_dense.h", "norm.hip", "gate.hip", "distill.hip")
+DENSE_SOURCES = ("tt_dense.h", "norm.hip", "gate.hip", "distill.hip",
+                 "tt_attend.h", "rotate.hip", "attend.hip", "paged.hip")
 
 
 def kernel_source_hash() -> str:

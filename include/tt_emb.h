@@ -435,6 +435,103 @@ tt_status tt_emb_distill_train(int32_t dtype, const void* logits, int64_t ld, co
                                void* dlogits, int64_t ldd, int64_t rows, int64_t classes, float temperature,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A layer's attention on looked-up rows: norms of queries and keys with the
+ * rotation by position, attention over whole packed prompts, and attention of
+ * one new token over a paged cache. Rows, types, workspaces and streams are as
+ * for the dense operators above. Heads lie side by side in a row: queries
+ * [rows][heads * dim], keys and values [rows][kv_heads * dim], each with a row
+ * stride of its own, so that they may be parts of one projection's output.
+ * heads is a multiple of kv_heads; query head h reads key head
+ * h / (heads / kv_heads). All sums, statistics and angles are held in fp32 or
+ * more; what is found bad in device data (offsets, slots, pages) is bounded by
+ * the kernels, so that nothing outside the buffers is read or written. */
+
+/* Which elements of a head form the pairs that are rotated, of the leading
+ * `rot`: p and p + rot/2, or 2p and 2p + 1. */
+typedef enum { TT_PAIRS_HALVES = 0, TT_PAIRS_NEIGHBOURS = 1 } tt_pairs;
+
+/* Of every head x of q and k: u = x / sqrt(mean(x^2) + eps) * weight, then its
+ * pairs (a, b) rotated by the angle positions[row] * freq[p] (formed in fp64):
+ *   (u_a cos - u_b sin, u_a sin + u_b cos); elements from rot on stay u.
+ *   wdtype  type of q_weight, k_weight [dim] and their gradients: dtype or TT_F32
+ *   positions  int64[rows];  freq  double[rot / 2], radians a position
+ * A head whose squares' sum overflows fp32 gives 0 (its infinite elements NaN).
+ * Limits: dim <= 256, heads, kv_heads <= 4096, rows <= 2^24. */
+size_t tt_emb_rotate_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim);
+tt_status tt_emb_rotate_forward(int32_t dtype, int32_t wdtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                const void* q_weight, const void* k_weight, const int64_t* positions,
+                                const double* freq, int64_t rot, int32_t pairs, void* q_out, int64_t ldqo, void* k_out,
+                                int64_t ldko, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, float eps,
+                                void* stream);
+
+/* The form that serves: as tt_emb_rotate_forward, but the rows' keys, and their
+ * values as they are, go into the paged cache: row r's to slot slots[r] of
+ * k_pages and v_pages, [num_slots][kv_heads * dim] (slot = page * page size +
+ * place in the page). A row whose slot is outside [0, num_slots) is kept
+ * nowhere (its q_out is written all the same); slots named twice hold either
+ * row's, in no order. */
+tt_status tt_emb_rotate_append(int32_t dtype, int32_t wdtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                               const void* v, int64_t ldv, const void* q_weight, const void* k_weight,
+                               const int64_t* positions, const double* freq, int64_t rot, int32_t pairs,
+                               const int64_t* slots, void* q_out, int64_t ldqo, void* k_pages, void* v_pages,
+                               int64_t num_slots, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim,
+                               float eps, void* stream);
+
+/* Gradients of tt_emb_rotate_forward in q, k and both weights. */
+tt_status tt_emb_rotate_backward(int32_t dtype, int32_t wdtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                 const void* q_weight, const void* k_weight, const int64_t* positions,
+                                 const double* freq, int64_t rot, int32_t pairs, const void* dq_out, int64_t lddqo,
+                                 const void* dk_out, int64_t lddko, void* dq, int64_t lddq, void* dk, int64_t lddk,
+                                 void* dq_weight, void* dk_weight, int64_t rows, int64_t heads, int64_t kv_heads,
+                                 int64_t dim, float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention over packed prompts. Sequence s is rows offsets[s] .. offsets[s+1]-1
+ * (int64 device array [seqs + 1], not decreasing, within [0, rows]); a row sees
+ * the rows of its own sequence, with causal != 0 those up to itself:
+ *   s_ij = scale q_i . k_j,  out_i = sum_j softmax_j(s_ij) v_j
+ * Rows of no sequence (before the first, behind the last) are neither read nor
+ * written. A score that is -inf counts as not seen; a row that sees nothing
+ * gives 0.
+ *   lse  float[heads][rows], log sum_j e^(s_ij), what the backward needs; NULL
+ *        when serving
+ * With 16-bit types the weights e^(s - max) are rounded to dtype before they
+ * meet v, and in the backward the weights and dout . v - dout . out times them
+ * before they meet the other factors; with TT_F16 the latter must lie in its
+ * range. Offsets that decrease or lie outside the rows leave the outputs
+ * unspecified. The workspace is the backward's.
+ * Limits: 0 < scale < inf; dim <= 128, rows < 2^31, row strides < 2^22,
+ * (rows / 32 + seqs) * heads <= 2^24. */
+size_t tt_emb_attend_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim);
+tt_status tt_emb_attend_forward(int32_t dtype, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                int64_t ldv, const int64_t* offsets, int64_t seqs, void* out, int64_t ldo, float* lse,
+                                int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, int32_t causal,
+                                float scale, void* stream);
+tt_status tt_emb_attend_backward(int32_t dtype, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                 int64_t ldv, const int64_t* offsets, int64_t seqs, const void* out, int64_t ldo,
+                                 const float* lse, const void* dout, int64_t lddo, void* dq, int64_t lddq, void* dk,
+                                 int64_t lddk, void* dv, int64_t lddv, int64_t rows, int64_t heads, int64_t kv_heads,
+                                 int64_t dim, int32_t causal, float scale, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Attention of one new token a sequence over its keys and values in the paged
+ * cache (k_pages, v_pages: [pages][page_size][kv_heads * dim]): token j of
+ * sequence s is place j % page_size of page table[s * ldt + j / page_size], for
+ * j < lengths[s] (int64; the new token's own key and value are in the cache
+ * already). A length past most_pages * page_size counts as that, one below zero
+ * as zero; a token whose page is outside [0, pages) is not seen; a sequence
+ * that sees nothing gives 0.
+ *   table  int32, most_pages entries a sequence, ldt apart
+ * The workspace serves any lengths, and fewer sequences.
+ * Limits: 0 < scale < inf; dim <= 128, heads / kv_heads <= 256,
+ * most_pages * page_size < 2^31, seqs * heads <= 2^20. */
+size_t tt_emb_attend_paged_workspace_bytes(int32_t dtype, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t dim);
+tt_status tt_emb_attend_paged(int32_t dtype, const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                              int64_t pages, int64_t page_size, const int32_t* table, int64_t ldt, int64_t most_pages,
+                              const int64_t* lengths, void* out, int64_t ldo, int64_t seqs, int64_t heads,
+                              int64_t kv_heads, int64_t dim, float scale, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* tt_emb_status_string(tt_status s);
 

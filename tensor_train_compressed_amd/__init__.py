@@ -30,6 +30,9 @@ __all__ = [
     "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
     "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward",
     "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train",
+    "tt_emb_rotate_workspace_bytes", "tt_emb_rotate_forward", "tt_emb_rotate_append", "tt_emb_rotate_backward",
+    "tt_emb_attend_workspace_bytes", "tt_emb_attend_forward", "tt_emb_attend_backward",
+    "tt_emb_attend_paged_workspace_bytes", "tt_emb_attend_paged",
     "EXPORTS",
 ]
 
@@ -57,6 +60,9 @@ EXPORTS = (
     "tt_emb_norm_workspace_bytes", "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_workspace_bytes",
     "tt_emb_gate_forward_workspace_bytes", "tt_emb_gate_forward", "tt_emb_gate_backward",
     "tt_emb_distill_workspace_bytes", "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train",
+    "tt_emb_rotate_workspace_bytes", "tt_emb_rotate_forward", "tt_emb_rotate_append", "tt_emb_rotate_backward",
+    "tt_emb_attend_workspace_bytes", "tt_emb_attend_forward", "tt_emb_attend_backward",
+    "tt_emb_attend_paged_workspace_bytes", "tt_emb_attend_paged",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -152,7 +158,7 @@ def load_library() -> ctypes.CDLL:
         lib.tt_emb_status_string.argtypes = [ctypes.c_int]
         lib.tt_emb_status_string.restype = ctypes.c_char_p
         sz, f32 = ctypes.c_size_t, ctypes.c_float
-        for op in ("norm", "gate", "gate_forward", "distill"):
+        for op in ("norm", "gate", "gate_forward", "distill", "rotate", "attend", "attend_paged"):
             getattr(lib, f"tt_emb_{op}_workspace_bytes").restype = sz
         lib.tt_emb_norm_workspace_bytes.argtypes = [i32, i64, i64]
         lib.tt_emb_gate_workspace_bytes.argtypes = [i32, i64, i64, i64]
@@ -166,13 +172,27 @@ def load_library() -> ctypes.CDLL:
         lib.tt_emb_distill_forward.argtypes = [i32, P, i64, P, P, i64, P, P, i64, i64, f32, P, sz, P]
         lib.tt_emb_distill_backward.argtypes = [i32, P, i64, P, P, i64, P, P, P, i64, i64, i64, f32, P]
         lib.tt_emb_distill_train.argtypes = [i32, P, i64, P, P, i64, P, P, P, i64, i64, i64, f32, P, sz, P]
+        for op in ("rotate", "attend", "attend_paged"):
+            getattr(lib, f"tt_emb_{op}_workspace_bytes").argtypes = [i32, i64, i64, i64, i64]
+        rows = [i64, i64, i64, i64]   # rows, heads, kv_heads, dim
+        lib.tt_emb_rotate_forward.argtypes = [i32, i32, P, i64, P, i64, P, P, P, P, i64, i32, P, i64, P, i64, *rows, f32, P]
+        lib.tt_emb_rotate_append.argtypes = [i32, i32, P, i64, P, i64, P, i64, P, P, P, P, i64, i32, P, P, i64, P, P, i64,
+                                             *rows, f32, P]
+        lib.tt_emb_rotate_backward.argtypes = [i32, i32, P, i64, P, i64, P, P, P, P, i64, i32, P, i64, P, i64, P, i64, P,
+                                               i64, P, P, *rows, f32, P, sz, P]
+        lib.tt_emb_attend_forward.argtypes = [i32, P, i64, P, i64, P, i64, P, i64, P, i64, P, *rows, i32, f32, P]
+        lib.tt_emb_attend_backward.argtypes = [i32, P, i64, P, i64, P, i64, P, i64, P, i64, P, P, i64, P, i64, P, i64, P,
+                                               i64, *rows, i32, f32, P, sz, P]
+        lib.tt_emb_attend_paged.argtypes = [i32, P, i64, P, P, i64, i64, P, i64, i64, P, P, i64, *rows, f32, P, sz, P]
         for name in ("tt_emb_plan", "tt_emb_forward", "tt_emb_forward_train", "tt_emb_backward",
                      "tt_emb_backward_kept", "tt_emb_sgd", "tt_emb_get_error", "tt_emb_plan_get_view",
                      "tt_emb_plan_counts", "tt_emb_plan_destroy", "tt_emb_query_paths",
                      "tt_emb_cache_build", "tt_emb_plan_cached", "tt_emb_forward_cached",
                      "tt_emb_backward_cached", "tt_emb_backward_sgd_cached",
                      "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_gate_forward", "tt_emb_gate_backward",
-                     "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train"):
+                     "tt_emb_distill_forward", "tt_emb_distill_backward", "tt_emb_distill_train",
+                     "tt_emb_rotate_forward", "tt_emb_rotate_append", "tt_emb_rotate_backward",
+                     "tt_emb_attend_forward", "tt_emb_attend_backward", "tt_emb_attend_paged"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -743,3 +763,152 @@ def tt_emb_distill_train(logits, ids, top_logits, row_weight, loss, dlogits, tem
         "tt_emb_distill_train", logits, stream,
         code, pz, ld, pi, pt, top, _dev_ptr(row_weight, "float32", "row_weight", rows),
         _dev_ptr(loss, "float32", "loss", rows), pd, ldd, rows, classes, float(temperature), pws, nws)
+
+
+# ---------------------------------------------------------------------------
+# A layer's attention on looked-up rows: norms of queries and keys with the
+# rotation by position, attention over packed prompts and over a paged cache.
+
+_PAIRS = {"halves": 0, "neighbours": 1}
+
+
+def _head_count(columns: int, dim: int, what: str) -> int:
+    n, rest = divmod(columns, dim) if dim > 0 else (0, columns)
+    if rest or n < 1:
+        raise ValueError(f"{what} has {columns} columns, not whole heads of {dim}")
+    return n
+
+
+def tt_emb_rotate_workspace_bytes(dtype, rows: int, heads: int, kv_heads: int, dim: int) -> int:
+    return int(load_library().tt_emb_rotate_workspace_bytes(_dtype_code(dtype, "dtype"), rows, heads, kv_heads, dim))
+
+
+def _rotate_sizes(q, k, q_weight, k_weight, positions, freq, pairs):
+    """The leading arguments of the rotation's calls, and (rows, heads, kv_heads, dim)."""
+    if pairs not in _PAIRS:
+        raise ValueError(f"pairs must be one of {', '.join(_PAIRS)}, got {pairs!r}")
+    code, wcode = _dtype_code(q.dtype, "q"), _dtype_code(q_weight.dtype, "q_weight")
+    pq, ldq = _matrix(q, q.dtype, "q")
+    rows = q.shape[0]
+    pk, ldk = _matrix(k, q.dtype, "k", rows)
+    dim = q_weight.numel()
+    wname = _name(q_weight.dtype)
+    sizes = rows, _head_count(q.shape[1], dim, "q"), _head_count(k.shape[1], dim, "k"), dim
+    return (code, wcode, pq, ldq, pk, ldk, _dev_ptr(q_weight, wname, "q_weight"),
+            _dev_ptr(k_weight, wname, "k_weight", dim), _dev_ptr(positions, "int64", "positions", rows),
+            _dev_ptr(freq, "float64", "freq"), 2 * freq.numel(), _PAIRS[pairs]), sizes
+
+
+def tt_emb_rotate_forward(q, k, q_weight, k_weight, positions, freq, q_out, k_out, pairs: str = "halves",
+                          eps: float = 1e-6, stream=None):
+    """Norms of every head of q [rows, heads * dim] and k [rows, kv_heads * dim], then their rotation by
+    positions (int64[rows]) times freq (float64[pairs of a head], radians a position)."""
+    args, (rows, heads, kv, dim) = _rotate_sizes(q, k, q_weight, k_weight, positions, freq, pairs)
+    _launch("tt_emb_rotate_forward", q, stream, *args, *_matrix(q_out, q.dtype, "q_out", rows, heads * dim),
+            *_matrix(k_out, q.dtype, "k_out", rows, kv * dim), rows, heads, kv, dim, float(eps))
+
+
+def _pages(k_pages, v_pages, dtype, heads_dim: Optional[int] = None):
+    """Both caches' data_ptr() and their shape [pages, page_size, kv_heads, dim]."""
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError(f"k_pages and v_pages must be [pages, page_size, kv_heads, dim], got {list(shape)} and "
+                         f"{list(v_pages.shape)}")
+    if heads_dim is not None and shape[2] * shape[3] != heads_dim:
+        raise ValueError(f"a token of the cache has {shape[2]} x {shape[3]} elements, k has {heads_dim}")
+    name = _name(dtype)
+    return _dev_ptr(k_pages, name, "k_pages"), _dev_ptr(v_pages, name, "v_pages"), shape
+
+
+def tt_emb_rotate_append(q, k, v, q_weight, k_weight, positions, freq, slots, q_out, k_pages, v_pages,
+                         pairs: str = "halves", eps: float = 1e-6, stream=None):
+    """tt_emb_rotate_forward whose keys, with the values v, go into the paged cache
+    [pages, page_size, kv_heads, dim], row r's to place slots[r] (int64) of all pages' in a row; rows whose
+    slot lies outside the cache are kept nowhere."""
+    args, (rows, heads, kv, dim) = _rotate_sizes(q, k, q_weight, k_weight, positions, freq, pairs)
+    pkp, pvp, shape = _pages(k_pages, v_pages, q.dtype, kv * dim)
+    _launch("tt_emb_rotate_append", q, stream, *args[:6], *_matrix(v, q.dtype, "v", rows, kv * dim), *args[6:],
+            _dev_ptr(slots, "int64", "slots", rows), *_matrix(q_out, q.dtype, "q_out", rows, heads * dim), pkp, pvp,
+            shape[0] * shape[1], rows, heads, kv, dim, float(eps))
+
+
+def tt_emb_rotate_backward(q, k, q_weight, k_weight, positions, freq, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+                           pairs: str = "halves", eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of tt_emb_rotate_forward."""
+    args, (rows, heads, kv, dim) = _rotate_sizes(q, k, q_weight, k_weight, positions, freq, pairs)
+    given = _matrix(dq_out, q.dtype, "dq_out", rows, heads * dim) + _matrix(dk_out, q.dtype, "dk_out", rows, kv * dim)
+    taken = _matrix(dq, q.dtype, "dq", rows, heads * dim) + _matrix(dk, q.dtype, "dk", rows, kv * dim)
+    wname = _name(q_weight.dtype)
+    ws, pws, nws = _workspace(workspace, tt_emb_rotate_workspace_bytes, (q.dtype, rows, heads, kv, dim),
+                              "tt_emb_rotate_backward", q, stream)
+    _launch("tt_emb_rotate_backward", q, stream, *args, *given, *taken, _dev_ptr(dq_weight, wname, "dq_weight", dim),
+            _dev_ptr(dk_weight, wname, "dk_weight", dim), rows, heads, kv, dim, float(eps), pws, nws)
+
+
+def tt_emb_attend_workspace_bytes(dtype, rows: int, heads: int, kv_heads: int, dim: int) -> int:
+    return int(load_library().tt_emb_attend_workspace_bytes(_dtype_code(dtype, "dtype"), rows, heads, kv_heads, dim))
+
+
+def _attend_sizes(q, k, v, offsets, heads, kv_heads, scale):
+    """The leading arguments of the attention's calls, (rows, heads, kv_heads, dim) and the scale."""
+    code = _dtype_code(q.dtype, "q")
+    pq, ldq = _matrix(q, q.dtype, "q")
+    rows, columns = q.shape
+    if heads < 1 or columns % heads or columns == 0:
+        raise ValueError(f"q has {columns} columns, not {heads} whole heads")
+    dim = columns // heads
+    pk, ldk = _matrix(k, q.dtype, "k", rows, kv_heads * dim)
+    pv, ldv = _matrix(v, q.dtype, "v", rows, kv_heads * dim)
+    seqs = offsets.numel() - 1
+    if seqs < 0:
+        raise ValueError("offsets must have one entry more than there are sequences")
+    return ((code, pq, ldq, pk, ldk, pv, ldv, _dev_ptr(offsets, "int64", "offsets"), seqs),
+            (rows, heads, kv_heads, dim), dim ** -0.5 if scale is None else float(scale))
+
+
+def tt_emb_attend_forward(q, k, v, offsets, out, lse=None, *, heads: int, kv_heads: int, causal: bool = True,
+                          scale: Optional[float] = None, stream=None):
+    """Attention of each packed sequence (rows offsets[s] to offsets[s + 1] of q [rows, heads * dim], k and v
+    [rows, kv_heads * dim]) into out; lse (float32 [heads, rows]) is kept for tt_emb_attend_backward when given.
+    scale: 1 / sqrt(dim) unless given."""
+    args, sizes, scale = _attend_sizes(q, k, v, offsets, heads, kv_heads, scale)
+    rows, _, _, dim = sizes
+    _launch("tt_emb_attend_forward", q, stream, *args, *_matrix(out, q.dtype, "out", rows, heads * dim),
+            _dev_ptr(lse, "float32", "lse", heads * rows), *sizes, int(bool(causal)), scale)
+
+
+def tt_emb_attend_backward(q, k, v, offsets, out, lse, dout, dq, dk, dv, *, heads: int, kv_heads: int,
+                           causal: bool = True, scale: Optional[float] = None, workspace=None, stream=None):
+    """Gradients of tt_emb_attend_forward from its out and the lse it kept."""
+    args, sizes, scale = _attend_sizes(q, k, v, offsets, heads, kv_heads, scale)
+    rows, _, _, dim = sizes
+    given = (*_matrix(out, q.dtype, "out", rows, heads * dim), _dev_ptr(lse, "float32", "lse", heads * rows),
+             *_matrix(dout, q.dtype, "dout", rows, heads * dim))
+    taken = (*_matrix(dq, q.dtype, "dq", rows, heads * dim), *_matrix(dk, q.dtype, "dk", rows, kv_heads * dim),
+             *_matrix(dv, q.dtype, "dv", rows, kv_heads * dim))
+    ws, pws, nws = _workspace(workspace, tt_emb_attend_workspace_bytes, (q.dtype, *sizes), "tt_emb_attend_backward", q,
+                              stream)
+    _launch("tt_emb_attend_backward", q, stream, *args, *given, *taken, *sizes, int(bool(causal)), scale, pws, nws)
+
+
+def tt_emb_attend_paged_workspace_bytes(dtype, seqs: int, heads: int, kv_heads: int, dim: int) -> int:
+    return int(load_library().tt_emb_attend_paged_workspace_bytes(_dtype_code(dtype, "dtype"), seqs, heads, kv_heads,
+                                                                  dim))
+
+
+def tt_emb_attend_paged(q, k_pages, v_pages, table, lengths, out, scale: Optional[float] = None, workspace=None,
+                        stream=None):
+    """Attention of one new token a sequence (q [seqs, heads * dim]) over its lengths[s] (int64) keys and values
+    in the paged cache [pages, page_size, kv_heads, dim]; table (int32 [seqs, most pages]) names its pages."""
+    code = _dtype_code(q.dtype, "q")
+    pq, ldq = _matrix(q, q.dtype, "q")
+    pkp, pvp, shape = _pages(k_pages, v_pages, q.dtype)
+    pages, page_size, kv, dim = shape
+    seqs, heads = q.shape[0], _head_count(q.shape[1], dim, "q")
+    import torch
+    pt, ldt = _matrix(table, torch.int32, "table", seqs)
+    ws, pws, nws = _workspace(workspace, tt_emb_attend_paged_workspace_bytes, (q.dtype, seqs, heads, kv, dim),
+                              "tt_emb_attend_paged", q, stream)
+    _launch("tt_emb_attend_paged", q, stream, code, pq, ldq, pkp, pvp, pages, page_size, pt, ldt, table.shape[1],
+            _dev_ptr(lengths, "int64", "lengths", seqs), *_matrix(out, q.dtype, "out", seqs, heads * dim), seqs, heads, kv,
+            dim, dim ** -0.5 if scale is None else float(scale), pws, nws)

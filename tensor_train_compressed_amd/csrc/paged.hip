@@ -1,0 +1,319 @@
+// Attention of one new token a sequence over its keys and values in a paged cache.
+//
+//   s_j = scale q . k_j,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
+//
+// Bound by memory: the cache is read once, by the workgroup that answers every head of a
+// key head (a wave's 32 columns are these heads). A sequence's tokens are split over
+// workgroups and, there, over waves, each with a softmax of its own; waves are joined in
+// LDS and workgroups, where a sequence has several, by a second launch, in a fixed order.
+#include "tt_attend.h"
+
+namespace tt {
+namespace {
+
+constexpr int kWaves = 4, kTokens = 32;           // tokens of a wave's tile
+constexpr int kHeads = 32;                        // heads of a workgroup at most
+constexpr int kMinChunk = 256;                    // tokens a workgroup takes, where there are that many
+
+struct PagedArgs {
+    const void *q, *k, *v;
+    int64_t ldq, pages, ldt, ldo;
+    const int32_t* table;
+    const int64_t* lengths;
+    void* out;
+    int page, most, seqs, heads, kv, group, blocks, splits, D;   // most: tokens of a sequence; blocks: of kHeads heads
+    float scale;
+    float* part;        // [seqs][heads][splits][DP], weighted sums
+    float2* ml;         // [seqs][heads][splits], maximum and sum of weights
+    hipStream_t s;
+};
+
+__device__ __forceinline__ int length_of(const PagedArgs& a, int seq) {
+    const int64_t n = a.lengths[seq];
+    return n < 0 ? 0 : n > a.most ? a.most : (int)n;
+}
+// Tokens of a workgroup.
+__device__ __forceinline__ int chunk_of(const PagedArgs& a, int len) {
+    const int n = (int)(((int64_t)len + a.splits - 1) / a.splits);
+    return max(kMinChunk, (n + kWaves * kTokens - 1) / (kWaves * kTokens) * (kWaves * kTokens));
+}
+
+template <class T, int DP>
+__global__ __launch_bounds__(kWaves * 64) void k_attend_paged(const PagedArgs a) {
+    typedef Tile<T, DP> L;
+    constexpr int N = kTokens * L::SLOTS / 64, BYTES = kTokens * L::ROW;
+    static_assert(2 * BYTES >= kHeads * DP * 4, "room for a wave's sums");
+    __shared__ __align__(16) char tiles[kWaves][2 * BYTES];
+    __shared__ float sm_m[kWaves][kHeads], sm_l[kWaves][kHeads];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int b = blockIdx.x;
+    const int kv = b % a.kv;
+    b /= a.kv;
+    const int block = b % a.blocks;
+    b /= a.blocks;
+    const int split = b % a.splits, seq = b / a.splits;
+    const int len = length_of(a, seq), chunk = chunk_of(a, len), used = max(1, (len + chunk - 1) / chunk);
+    if (split >= used) return;
+    const int begin = split * chunk, end = min(len, begin + chunk);
+    const int heads = min(kHeads, a.group - block * kHeads), head0 = kv * a.group + block * kHeads;
+    const float c = a.scale * kLog2e;
+
+    Piece fq[L::STEPS];
+    load_row<T, DP>(fq, (const T*)a.q + seq * a.ldq + (int64_t)(head0 + (lane & 31)) * a.D, (lane & 31) < heads, a.D);
+    const int32_t* table = a.table + seq * a.ldt;
+    // the cache's row of token t0 + lane % 32, or -1
+    auto row_of = [&](int t0) -> int64_t {
+        const int t = t0 + (lane & 31);
+        if (t >= end) return -1;
+        const int64_t p = table[t / a.page];
+        return p >= 0 && p < a.pages ? p * a.page + t % a.page : -1;
+    };
+    Piece rk[N], rv[N];
+    uint32_t seen = 0;           // of the tile in rk and rv
+    auto load = [&](int t0) {
+        const int64_t row = row_of(t0);
+        seen = (uint32_t)__ballot(row >= 0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = (i * 64 + lane) / L::SLOTS, piece = ((i * 64 + lane) % L::SLOTS) ^ L::key(r), e = piece * L::P;
+            const int64_t at = __shfl(row, r) * a.kv + kv;
+            const int n = seen >> r & 1 ? max(0, min(L::P, a.D - e)) : 0;
+            rk[i] = load_piece((const T*)a.k + at * a.D + e, n);
+            rv[i] = load_piece((const T*)a.v + at * a.D + e, n);
+        }
+    };
+    char *sk = tiles[wave], *sv = sk + BYTES;
+    floatx16 o[DP / 32] = {};
+    Softmax<T> sm;
+    sm.init();
+    int t0 = begin + wave * kTokens;
+    if (t0 < end) load(t0);
+    for (; t0 < end; t0 += kWaves * kTokens) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            *reinterpret_cast<Piece*>(sk + (i * 64 + lane) * 16) = rk[i];
+            *reinterpret_cast<Piece*>(sv + (i * 64 + lane) * 16) = rv[i];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        const uint32_t here = seen;
+        if (t0 + kWaves * kTokens < end) load(t0 + kWaves * kTokens);
+        floatx16 s[1] = {};
+#pragma unroll
+        for (int x = 0; x < L::STEPS; ++x) s[0] = mma_rows<T>(L::row_piece(sk, 0, x), fq[x], s[0]);
+        if (here != ~0u) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (!(here >> block_row(r) & 1)) s[0][r] = -INFINITY;
+        }
+        sm.step(s, c, [&](float f) {
+#pragma unroll
+            for (int j = 0; j < DP / 32; ++j) o[j] *= f;
+        });
+        Weights<T> w;
+        w.set(s[0]);
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) o[j] = mma_columns<T, DP>(sv, 0, j, w, o[j]);
+    }
+
+    // the waves' sums, joined at the largest maximum; a head's row of sums lies in LDS in
+    // 16-byte pieces in the order piece ^ head
+    const float total = sm.total();
+    if (lane < kHeads) {
+        sm_m[wave][lane] = sm.m;
+        sm_l[wave][lane] = total;
+    }
+    __syncthreads();
+    const int h = lane & 31;
+    constexpr int KEY = (DP % 64 == 0 ? 16 : 8) - 1;   // (orders within 16 or 8 pieces, of which a row has whole lots)
+    {
+        float top = sm_m[0][h];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm_m[w][h]);
+        const float f = Softmax<T>::moved(sm.m, top, c);
+        if (h < heads) {
+            char* p = tiles[wave] + h * DP * 4;
+#pragma unroll
+            for (int j = 0; j < DP / 32; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float4 v = make_float4(o[j][4 * g] * f, o[j][4 * g + 1] * f, o[j][4 * g + 2] * f,
+                                                 o[j][4 * g + 3] * f);
+                    *reinterpret_cast<float4*>(p + (((32 * j + block_row(4 * g)) / 4) ^ (h & KEY)) * 16) = v;
+                }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * (DP / 4); i += kWaves * 64) {
+        const int n = i / (DP / 4), d = i % (DP / 4) * 4;
+        float top = sm_m[0][n], l = 0.f, v[4] = {};
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm_m[w][n]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            l += sm_l[w][n] * Softmax<T>::moved(sm_m[w][n], top, c);
+            const float4 x = *reinterpret_cast<const float4*>(tiles[w] + n * DP * 4 + ((d / 4) ^ (n & KEY)) * 16);
+            v[0] += x.x;
+            v[1] += x.y;
+            v[2] += x.z;
+            v[3] += x.w;
+        }
+        if (used == 1) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= inv;
+            store4n((T*)a.out + seq * a.ldo + (int64_t)(head0 + n) * a.D + d, v, a.D - d);
+        } else {
+            const int64_t at = ((int64_t)seq * a.heads + head0 + n) * a.splits + split;
+            *reinterpret_cast<float4*>(a.part + at * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
+            if (d == 0) a.ml[at] = make_float2(top, l);
+        }
+    }
+}
+
+// Joins the workgroups of a sequence's head.
+template <class T, int DP>
+__global__ __launch_bounds__(256) void k_attend_paged_join(const PagedArgs a) {
+    constexpr int LANES = DP / 4, ROWS = 256 / LANES;   // splits at a time
+    __shared__ float4 sm_v[256];
+    __shared__ float sm_m[256], sm_l[256];
+    const int seq = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    const int len = length_of(a, seq), chunk = chunk_of(a, len), used = max(1, (len + chunk - 1) / chunk);
+    if (used == 1) return;
+    const int64_t at = (int64_t)blockIdx.x * a.splits;
+    const float c = a.scale * kLog2e;
+    const int x = threadIdx.x % LANES, y = threadIdx.x / LANES;
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < used; i += 256) top = fmaxf(top, a.ml[at + i].x);
+    sm_m[threadIdx.x] = top;
+    __syncthreads();
+    for (int i = 128; i > 0; i /= 2) {
+        if ((int)threadIdx.x < i) sm_m[threadIdx.x] = fmaxf(sm_m[threadIdx.x], sm_m[threadIdx.x + i]);
+        __syncthreads();
+    }
+    top = sm_m[0];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (y < ROWS) {
+#pragma unroll 4
+        for (int i = y; i < used; i += ROWS) {
+            const float2 ml = a.ml[at + i];
+            const float f = Softmax<T>::moved(ml.x, top, c);
+            const float4 o = *reinterpret_cast<const float4*>(a.part + (at + i) * DP + x * 4);
+            v.x = fmaf(o.x, f, v.x);
+            v.y = fmaf(o.y, f, v.y);
+            v.z = fmaf(o.z, f, v.z);
+            v.w = fmaf(o.w, f, v.w);
+            l = fmaf(ml.y, f, l);
+        }
+    }
+    sm_v[threadIdx.x] = v;
+    sm_l[threadIdx.x] = l;
+    __syncthreads();
+    if (threadIdx.x >= LANES) return;
+    float r[4] = {};
+    l = 0.f;
+    for (int i = 0; i < ROWS; ++i) {
+        const float4 o = sm_v[i * LANES + x];
+        r[0] += o.x;
+        r[1] += o.y;
+        r[2] += o.z;
+        r[3] += o.w;
+        l += sm_l[i * LANES + x];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] *= inv;
+    store4n((T*)a.out + seq * a.ldo + (int64_t)head * a.D + x * 4, r, a.D - x * 4);
+}
+
+// Workgroups that a call is split to reach, and the splits of a sequence at most.
+constexpr int64_t kGroups = 2048, kMaxSplits = 512;
+
+inline int64_t padded_dim(int64_t dim) { return (dim + 31) / 32 * 32; }
+
+template <class T, int DP>
+tt_status paged_launch(const PagedArgs& a) {
+    const unsigned grid = (unsigned)((int64_t)a.seqs * a.splits * a.blocks * a.kv);
+    TT_LAUNCH(nullptr, "k_attend_paged", a.s, (k_attend_paged<T, DP>), dim3(grid), dim3(kWaves * 64), 0, a.s, a);
+    TT_LAUNCH_CHECK();
+    if (a.splits > 1) {
+        TT_LAUNCH(nullptr, "k_attend_paged_join", a.s, (k_attend_paged_join<T, DP>), dim3(a.seqs * a.heads), dim3(256), 0,
+                  a.s, a);
+        TT_LAUNCH_CHECK();
+    }
+    return TT_OK;
+}
+
+template <class T>
+tt_status paged_by_dim(const PagedArgs& a) {
+    if (a.D <= 32) return paged_launch<T, 32>(a);
+    if (a.D <= 64) return paged_launch<T, 64>(a);
+    if (a.D <= 96) return paged_launch<T, 96>(a);
+    return paged_launch<T, 128>(a);
+}
+
+tt_status paged_sizes(int32_t dtype, int64_t seqs, int64_t heads, int64_t kv, int64_t dim) {
+    if (!dtype_ok(dtype) || seqs < 0 || heads < 1 || kv < 1 || dim < 1 || heads % kv != 0) return TT_ERR_INVALID_ARG;
+    if (dim > 128 || heads / kv > 256 || heads > (int64_t(1) << 20) || seqs > (int64_t(1) << 20) ||
+        seqs * heads > int64_t(1) << 20)
+        return TT_ERR_UNSUPPORTED;
+    return TT_OK;
+}
+
+inline int64_t head_blocks(int64_t heads, int64_t kv) { return (heads / kv + kHeads - 1) / kHeads; }
+
+}  // namespace
+}  // namespace tt
+
+using namespace tt;
+
+extern "C" size_t tt_emb_attend_paged_workspace_bytes(int32_t dtype, int64_t seqs, int64_t heads, int64_t kv_heads,
+                                                      int64_t dim) {
+    if (paged_sizes(dtype, seqs, heads, kv_heads, dim) != TT_OK) return 0;
+    // n sequences are cut into at most 1 + kGroups / (n kv_heads blocks) splits each, kMaxSplits at most
+    const int64_t parts =
+        heads * std::min(seqs * kMaxSplits, seqs + kGroups / (kv_heads * head_blocks(heads, kv_heads)));
+    return std::max<size_t>(256, ((size_t)parts * (padded_dim(dim) + 2) * sizeof(float) + 511) & ~size_t(255));
+}
+
+extern "C" tt_status tt_emb_attend_paged(int32_t dtype, const void* q, int64_t ldq, const void* k_pages,
+                                         const void* v_pages, int64_t pages, int64_t page_size, const int32_t* table,
+                                         int64_t ldt, int64_t most_pages, const int64_t* lengths, void* out,
+                                         int64_t ldo, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t dim,
+                                         float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    const tt_status st = paged_sizes(dtype, seqs, heads, kv_heads, dim);
+    if (st != TT_OK) return st;
+    if (pages < 0 || page_size < 1 || most_pages < 0 || ldt < most_pages || !(scale > 0.f && scale < INFINITY))
+        return TT_ERR_INVALID_ARG;
+    if (ldq < heads * dim || ldo < heads * dim) return TT_ERR_INVALID_ARG;
+    if (seqs > 0 && (!q || !out || !lengths || (most_pages > 0 && !table) || (pages > 0 && (!k_pages || !v_pages))))
+        return TT_ERR_INVALID_ARG;
+    if (page_size > INT32_MAX || most_pages > INT32_MAX || most_pages * page_size > INT32_MAX || pages > INT32_MAX)
+        return TT_ERR_UNSUPPORTED;
+    if (!workspace || ((uintptr_t)workspace & 255) != 0) return TT_ERR_INVALID_ARG;
+    if (workspace_bytes < tt_emb_attend_paged_workspace_bytes(dtype, seqs, heads, kv_heads, dim))
+        return TT_ERR_WORKSPACE;
+    if (seqs == 0) return TT_OK;
+    PagedArgs a{};
+    a.q = q; a.k = k_pages; a.v = v_pages;
+    a.ldq = ldq; a.pages = pages; a.ldt = ldt; a.ldo = ldo;
+    a.table = table; a.lengths = lengths; a.out = out;
+    a.page = (int)page_size; a.most = (int)(most_pages * page_size);
+    a.seqs = (int)seqs; a.heads = (int)heads; a.kv = (int)kv_heads;
+    a.group = (int)(heads / kv_heads); a.blocks = (int)head_blocks(heads, kv_heads);
+    a.D = (int)dim;
+    const int64_t n = seqs * kv_heads * a.blocks;
+    const int64_t cuts = std::min(kMaxSplits, (kGroups + n - 1) / n);
+    a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(cuts, ((int64_t)a.most + kMinChunk - 1) / kMinChunk));
+    a.scale = scale;
+    a.part = (float*)workspace;
+    a.ml = (float2*)(a.part + seqs * heads * a.splits * padded_dim(dim));
+    a.s = (hipStream_t)stream;
+    if (dtype == TT_F32) return paged_by_dim<float>(a);
+    if (dtype == TT_BF16) return paged_by_dim<bf16>(a);
+    return paged_by_dim<f16>(a);
+}
