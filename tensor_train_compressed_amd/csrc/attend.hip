@@ -37,6 +37,9 @@ struct AttendArgs {
     hipStream_t s;
 };
 
+// Lambdas of a kernel's loop are part of it, whatever their size.
+#define TT_INLINE __attribute__((always_inline))
+
 constexpr int kQueries = 32;   // a wave's
 
 // Rows of a tile that goes through LDS, and waves of a workgroup.
@@ -45,6 +48,15 @@ constexpr int tile_rows() {
     return Tile<T, DP>::ROW <= 256 ? 64 : 32;
 }
 constexpr int kWaves = 4;
+
+// Waves a SIMD is to hold: two where their registers allow it without spilling.
+enum Pass { FWD, DQ, DKV };
+template <class T, int DP, bool DMA, Pass PASS>
+constexpr int waves_of() {
+    if (sizeof(T) == 4) return DP == 32 || (DP == 64 && DMA && PASS != DKV) ? 2 : 1;
+    if (PASS == DKV) return DP <= 64 || (DP == 96 && DMA) ? 2 : 1;
+    return DP <= 96 || DMA ? 2 : 1;
+}
 
 // The workgroup's head (its key head): those of one key head next to each other.
 struct Job {
@@ -56,11 +68,11 @@ __device__ __forceinline__ Job job_of(const AttendArgs& a) {
     return {(int64_t)(blockIdx.x / a.heads), kv, kv * (a.heads / a.kv) + i / a.kv};
 }
 
-template <class T, int DP>
-__global__ __launch_bounds__(kWaves * 64) void k_attend(const AttendArgs a) {
+template <class T, int DP, bool DMA>
+__global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, FWD>())) void k_attend(const AttendArgs a) {
     typedef Tile<T, DP> L;
     constexpr int BN = tile_rows<T, DP>(), BLOCKS = BN / 32, BM = kWaves * kQueries;
-    __shared__ __align__(16) char sk[BN * L::ROW], sv[BN * L::ROW];
+    __shared__ __align__(16) char sk0[BN * L::ROW], sv0[BN * L::ROW], sk1[BN * L::ROW], sv1[BN * L::ROW];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Job job = job_of(a);
     Span sp;
@@ -68,54 +80,66 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend(const AttendArgs a) {
     const int first = (sp.tiles - 1 - sp.tile) * BM, q0 = first + wave * kQueries, qi = q0 + (lane & 31);
     const bool there = qi < sp.len;
     const int64_t row = sp.first + qi;
-    Piece fq[L::STEPS];
-    load_row<T, DP>(fq, (const T*)a.q + row * a.ldq + (int64_t)job.head * a.D, there, a.D);
     const T* pk = (const T*)a.k + sp.first * a.ldk + (int64_t)job.kv * a.D;
     const T* pv = (const T*)a.v + sp.first * a.ldv + (int64_t)job.kv * a.D;
     const int last = a.causal ? min(sp.len, first + BM) : sp.len;              // of the workgroup's keys
     const int mine = a.causal ? min(sp.len, q0 + kQueries) : sp.len;           // of this wave's
     const int whole = a.causal ? min(sp.len, q0 + 1) : sp.len;                 // seen by all of its queries
     const int limit = a.causal ? min(sp.len, qi + 1) : sp.len;                 // seen by this lane's
+    TileLoad<T, DP, BN, kWaves, DMA> lk, lv;
+    lk.init(a.ldk, a.D, wave);
+    lv.init(a.ldv, a.D, wave);
+    lk.issue(sk0, pk, sp.len);
+    lv.issue(sv0, pv, sp.len);
+    Piece fq[L::STEPS];
+    load_row<T, DP>(fq, (const T*)a.q + row * a.ldq + (int64_t)job.head * a.D, there, a.D);
     const float c = a.scale * kLog2e;
     floatx16 o[DP / 32] = {};
     Softmax<T> sm;
     sm.init();
-    TileLoad<T, DP, BN, kWaves * 64> lk, lv;
-    lk.load(pk, a.ldk, sp.len, a.D);
-    lv.load(pv, a.ldv, sp.len, a.D);
-    for (int k0 = 0; k0 < last; k0 += BN) {
-        __syncthreads();
-        lk.store(sk);
-        lv.store(sv);
-        __syncthreads();
-        if (k0 + BN < last) {
-            lk.load(pk + (k0 + BN) * a.ldk, a.ldk, sp.len - k0 - BN, a.D);
-            lv.load(pv + (k0 + BN) * a.ldv, a.ldv, sp.len - k0 - BN, a.D);
+    lk.store(sk0);
+    lv.store(sv0);
+    // the tile of keys from k0 on, in (sk, sv); the next one's loads to (tk, tv)
+    auto step = [&](int k0, const char* sk, const char* sv, char* tk, char* tv) TT_INLINE {
+        landed_barrier();
+        const int next = k0 + BN;
+        if (next < last) {
+            lk.issue(tk, pk + next * a.ldk, sp.len - next);
+            lv.issue(tv, pv + next * a.ldv, sp.len - next);
         }
-        if (k0 >= mine) continue;
-        floatx16 s[BLOCKS] = {};
+        if (k0 < mine) {
+            floatx16 s[BLOCKS] = {};
 #pragma unroll
-        for (int x = 0; x < L::STEPS; ++x)
+            for (int x = 0; x < L::STEPS; ++x)
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) s[b] = mma_rows<T>(L::row_piece(sk, 32 * b, x), fq[x], s[b]);
-        if (k0 + BN > whole) {
+                for (int b = 0; b < BLOCKS; ++b) s[b] = mma_rows<T>(L::row_piece(sk, 32 * b, x), fq[x], s[b]);
+            if (next > whole) {
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b)
+                for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (k0 + 32 * b + block_row(r) >= limit) s[b][r] = -INFINITY;
+                    for (int r = 0; r < 16; ++r)
+                        if (k0 + 32 * b + block_row(r) >= limit) s[b][r] = -INFINITY;
+            }
+            sm.step(s, c, [&](float f) TT_INLINE {
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) o[j] *= f;
+            });
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                Weights<T> w;
+                w.set(s[b]);
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) o[j] = mma_columns<T, DP>(sv, 32 * b, j, w, o[j]);
+            }
         }
-        sm.step(s, c, [&](float f) {
-#pragma unroll
-            for (int j = 0; j < DP / 32; ++j) o[j] *= f;
-        });
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-            Weights<T> w;
-            w.set(s[b]);
-#pragma unroll
-            for (int j = 0; j < DP / 32; ++j) o[j] = mma_columns<T, DP>(sv, 32 * b, j, w, o[j]);
+        if (next < last) {
+            lk.store(tk);
+            lv.store(tv);
         }
+    };
+    for (int k0 = 0; k0 < last; k0 += 2 * BN) {
+        step(k0, sk0, sv0, sk1, sv1);
+        if (k0 + BN < last) step(k0 + BN, sk1, sv1, sk0, sv0);
     }
     const float total = sm.total();
     if (!there) return;
@@ -128,19 +152,29 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend(const AttendArgs a) {
 __device__ __forceinline__ float log2_sum(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
 // dq, and delta for the kernel below: by queries, as the forward.
-template <class T, int DP>
-__global__ __launch_bounds__(kWaves * 64) void k_attend_dq(const AttendArgs a) {
+template <class T, int DP, bool DMA>
+__global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, DQ>())) void k_attend_dq(const AttendArgs a) {
     typedef Tile<T, DP> L;
     constexpr int BN = tile_rows<T, DP>(), BLOCKS = BN / 32, BM = kWaves * kQueries;
-    __shared__ __align__(16) char sk[BN * L::ROW], sv[BN * L::ROW];
+    __shared__ __align__(16) char sk0[BN * L::ROW], sv0[BN * L::ROW], sk1[BN * L::ROW], sv1[BN * L::ROW];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Job job = job_of(a);
     Span sp;
     if (!find_tile(a.offsets, a.seqs, a.rows, BM, job.tile, sp)) return;
     const int first = (sp.tiles - 1 - sp.tile) * BM, q0 = first + wave * kQueries, qi = q0 + (lane & 31);
     const bool there = qi < sp.len;
-    const int64_t row = sp.first + qi;
-    const int64_t at = (int64_t)job.head * a.D;
+    const int64_t row = sp.first + qi, at = (int64_t)job.head * a.D;
+    const T* pk = (const T*)a.k + sp.first * a.ldk + (int64_t)job.kv * a.D;
+    const T* pv = (const T*)a.v + sp.first * a.ldv + (int64_t)job.kv * a.D;
+    const int last = a.causal ? min(sp.len, first + BM) : sp.len;
+    const int mine = a.causal ? min(sp.len, q0 + kQueries) : sp.len;
+    const int whole = a.causal ? min(sp.len, q0 + 1) : sp.len;
+    const int limit = a.causal ? min(sp.len, qi + 1) : sp.len;
+    TileLoad<T, DP, BN, kWaves, DMA> lk, lv;
+    lk.init(a.ldk, a.D, wave);
+    lv.init(a.ldv, a.D, wave);
+    lk.issue(sk0, pk, sp.len);
+    lv.issue(sv0, pv, sp.len);
     Piece fq[L::STEPS], fd[L::STEPS];
     load_row<T, DP>(fq, (const T*)a.q + row * a.ldq + at, there, a.D);
     load_row<T, DP>(fd, (const T*)a.dout + row * a.lddo + at, there, a.D);
@@ -163,58 +197,58 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_dq(const AttendArgs a) {
         lse2 = log2_sum(a.lse[(int64_t)job.head * a.rows + row]);
         if (lane < 32) a.delta[(int64_t)job.head * a.rows + row] = delta;
     }
-    const T* pk = (const T*)a.k + sp.first * a.ldk + (int64_t)job.kv * a.D;
-    const T* pv = (const T*)a.v + sp.first * a.ldv + (int64_t)job.kv * a.D;
-    const int last = a.causal ? min(sp.len, first + BM) : sp.len;
-    const int mine = a.causal ? min(sp.len, q0 + kQueries) : sp.len;
-    const int whole = a.causal ? min(sp.len, q0 + 1) : sp.len;
-    const int limit = a.causal ? min(sp.len, qi + 1) : sp.len;
     const float c = a.scale * kLog2e;
     floatx16 dq[DP / 32] = {};
-    TileLoad<T, DP, BN, kWaves * 64> lk, lv;
-    lk.load(pk, a.ldk, sp.len, a.D);
-    lv.load(pv, a.ldv, sp.len, a.D);
-    for (int k0 = 0; k0 < last; k0 += BN) {
-        __syncthreads();
-        lk.store(sk);
-        lv.store(sv);
-        __syncthreads();
-        if (k0 + BN < last) {
-            lk.load(pk + (k0 + BN) * a.ldk, a.ldk, sp.len - k0 - BN, a.D);
-            lv.load(pv + (k0 + BN) * a.ldv, a.ldv, sp.len - k0 - BN, a.D);
+    lk.store(sk0);
+    lv.store(sv0);
+    auto step = [&](int k0, const char* sk, const char* sv, char* tk, char* tv) TT_INLINE {
+        landed_barrier();
+        const int next = k0 + BN;
+        if (next < last) {
+            lk.issue(tk, pk + next * a.ldk, sp.len - next);
+            lv.issue(tv, pv + next * a.ldv, sp.len - next);
         }
-        if (k0 >= mine) continue;
+        if (k0 < mine) {
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-            floatx16 s = {}, dp = {};
+            for (int b = 0; b < BLOCKS; ++b) {
+                floatx16 s = {}, dp = {};
 #pragma unroll
-            for (int x = 0; x < L::STEPS; ++x) {
-                s = mma_rows<T>(L::row_piece(sk, 32 * b, x), fq[x], s);
-                dp = mma_rows<T>(L::row_piece(sv, 32 * b, x), fd[x], dp);
+                for (int x = 0; x < L::STEPS; ++x) {
+                    s = mma_rows<T>(L::row_piece(sk, 32 * b, x), fq[x], s);
+                    dp = mma_rows<T>(L::row_piece(sv, 32 * b, x), fd[x], dp);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = exp2_hw(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
+                if (k0 + 32 * (b + 1) > whole) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (k0 + 32 * b + block_row(r) >= limit) s[r] = 0.f;
+                }
+                Weights<T> w;
+                w.set(s);
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) dq[j] = mma_columns<T, DP>(sk, 32 * b, j, w, dq[j]);
             }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = exp2_hw(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
-            if (k0 + 32 * (b + 1) > whole) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (k0 + 32 * b + block_row(r) >= limit) s[r] = 0.f;
-            }
-            Weights<T> w;
-            w.set(s);
-#pragma unroll
-            for (int j = 0; j < DP / 32; ++j) dq[j] = mma_columns<T, DP>(sk, 32 * b, j, w, dq[j]);
         }
+        if (next < last) {
+            lk.store(tk);
+            lv.store(tv);
+        }
+    };
+    for (int k0 = 0; k0 < last; k0 += 2 * BN) {
+        step(k0, sk0, sv0, sk1, sv1);
+        if (k0 + BN < last) step(k0 + BN, sk1, sv1, sk0, sv0);
     }
     if (there) store_columns<T, DP>((T*)a.dq + row * a.lddq + at, dq, a.scale, a.D);
 }
 
 // dk and dv: a wave keeps 32 keys and goes over the queries of every head that reads them.
-template <class T, int DP>
-__global__ __launch_bounds__(kWaves * 64) void k_attend_dkv(const AttendArgs a) {
+template <class T, int DP, bool DMA>
+__global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, DKV>())) void k_attend_dkv(const AttendArgs a) {
     typedef Tile<T, DP> L;
     constexpr int BM = tile_rows<T, DP>(), BLOCKS = BM / 32, BN = kWaves * kQueries;
-    __shared__ __align__(16) char sq[BM * L::ROW], sd[BM * L::ROW];
-    __shared__ __align__(16) float slse[BM], sdelta[BM];
+    __shared__ __align__(16) char sq0[BM * L::ROW], sd0[BM * L::ROW], sq1[BM * L::ROW], sd1[BM * L::ROW];
+    __shared__ __align__(16) float st0[2 * BM], st1[2 * BM];   // a tile's lse (in powers of two), then its delta
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kv = blockIdx.x % a.kv, group = a.heads / a.kv;
     Span sp;
@@ -222,38 +256,40 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_dkv(const AttendArgs a) 
     const int first = sp.tile * BN, k0 = first + wave * kQueries, ki = k0 + (lane & 31);
     const bool there = ki < sp.len;
     const int64_t row = sp.first + ki, at = (int64_t)kv * a.D;
+    const int begin = a.causal ? first / BM : 0, per = (sp.len + BM - 1) / BM - begin;   // tiles of queries a head
+    const int all = per * group;
+    TileLoad<T, DP, BM, kWaves, DMA> lq, ld;
+    lq.init(a.ldq, a.D, wave);
+    ld.init(a.lddo, a.D, wave);
+    float stat = 0.f;   // of query threadIdx.x % BM of the tile
+    auto issue = [&](int i, char* tq, char* td) TT_INLINE {
+        const int head = kv * group + i / per, q0 = (begin + i % per) * BM, left = sp.len - q0;
+        const int64_t r = sp.first + q0;
+        lq.issue(tq, (const T*)a.q + r * a.ldq + (int64_t)head * a.D, left);
+        ld.issue(td, (const T*)a.dout + r * a.lddo + (int64_t)head * a.D, left);
+        const int x = threadIdx.x % BM;
+        const bool is_delta = threadIdx.x >= BM;
+        stat = is_delta ? 0.f : INFINITY;
+        if (threadIdx.x < 2 * BM && x < left) {
+            const float f = (is_delta ? a.delta : a.lse)[(int64_t)head * a.rows + r + x];
+            stat = is_delta ? f : log2_sum(f);
+        }
+    };
+    auto store = [&](char* tq, char* td, float* ts) TT_INLINE {
+        lq.store(tq);
+        ld.store(td);
+        if (threadIdx.x < 2 * BM) ts[threadIdx.x] = stat;
+    };
+    issue(0, sq0, sd0);
     Piece fk[L::STEPS], fv[L::STEPS];
     load_row<T, DP>(fk, (const T*)a.k + row * a.ldk + at, there, a.D);
     load_row<T, DP>(fv, (const T*)a.v + row * a.ldv + at, there, a.D);
     const float c = a.scale * kLog2e;
     floatx16 dk[DP / 32] = {}, dv[DP / 32] = {};
-    const int begin = a.causal ? first / BM : 0, per = (sp.len + BM - 1) / BM - begin;   // tiles of queries a head
-    const int all = per * group;
-    TileLoad<T, DP, BM, kWaves * 64> lq, ld;
-    float l = INFINITY, d = 0.f;   // of query threadIdx.x of the tile
-    auto load = [&](int i) {
-        const int head = kv * group + i / per, q0 = (begin + i % per) * BM, left = sp.len - q0;
-        const int64_t r = sp.first + q0;
-        lq.load((const T*)a.q + r * a.ldq + (int64_t)head * a.D, a.ldq, left, a.D);
-        ld.load((const T*)a.dout + r * a.lddo + (int64_t)head * a.D, a.lddo, left, a.D);
-        l = INFINITY;
-        d = 0.f;
-        if ((int)threadIdx.x < BM && (int)threadIdx.x < left) {
-            l = log2_sum(a.lse[(int64_t)head * a.rows + r + threadIdx.x]);
-            d = a.delta[(int64_t)head * a.rows + r + threadIdx.x];
-        }
-    };
-    load(0);
-    for (int i = 0; i < all; ++i) {
-        __syncthreads();
-        lq.store(sq);
-        ld.store(sd);
-        if (threadIdx.x < BM) {
-            slse[threadIdx.x] = l;
-            sdelta[threadIdx.x] = d;
-        }
-        __syncthreads();
-        if (i + 1 < all) load(i + 1);
+    store(sq0, sd0, st0);
+    auto step = [&](int i, const char* sq, const char* sd, const float* st, char* tq, char* td, float* ts) TT_INLINE {
+        landed_barrier();
+        if (i + 1 < all) issue(i + 1, tq, td);
         const int q0 = (begin + i % per) * BM;
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
@@ -269,8 +305,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_dkv(const AttendArgs a) 
             for (int g = 0; g < 4; ++g) {
                 float lg[4], dg[4];
                 const int q = 32 * b + block_row(4 * g);
-                __builtin_memcpy(lg, slse + q, 16);
-                __builtin_memcpy(dg, sdelta + q, 16);
+                __builtin_memcpy(lg, st + q, 16);
+                __builtin_memcpy(dg, st + BM + q, 16);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = 4 * g + e;
@@ -293,24 +329,38 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_dkv(const AttendArgs a) 
 #pragma unroll
             for (int j = 0; j < DP / 32; ++j) dk[j] = mma_columns<T, DP>(sq, 32 * b, j, w, dk[j]);
         }
+        if (i + 1 < all) store(tq, td, ts);
+    };
+    for (int i = 0; i < all; i += 2) {
+        step(i, sq0, sd0, st0, sq1, sd1, st1);
+        if (i + 1 < all) step(i + 1, sq1, sd1, st1, sq0, sd0, st0);
     }
     if (!there) return;
     store_columns<T, DP>((T*)a.dk + row * a.lddk + at, dk, a.scale, a.D);
     store_columns<T, DP>((T*)a.dv + row * a.lddv + at, dv, 1.f, a.D);
 }
 
+// Whether rows start at whole 16-byte pieces, and their heads are made of them.
+bool pieces(const void* p, int64_t ld, int D, size_t size) {
+    return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && D * size % 16 == 0;
+}
+
 template <class T, int DP>
 tt_status attend_launch(const AttendArgs& a, bool backward) {
+    const bool keys = pieces(a.k, a.ldk, a.D, sizeof(T)) && pieces(a.v, a.ldv, a.D, sizeof(T));
     const int64_t tiles = a.rows / (kWaves * kQueries) + a.seqs;
     const dim3 grid((unsigned)(tiles * a.heads)), block(kWaves * 64);
     if (!backward) {
-        TT_LAUNCH(nullptr, "k_attend", a.s, (k_attend<T, DP>), grid, block, 0, a.s, a);
+        TT_LAUNCH(nullptr, "k_attend", a.s, (keys ? k_attend<T, DP, true> : k_attend<T, DP, false>), grid, block, 0, a.s, a);
         TT_LAUNCH_CHECK();
         return TT_OK;
     }
-    TT_LAUNCH(nullptr, "k_attend_dq", a.s, (k_attend_dq<T, DP>), grid, block, 0, a.s, a);
+    const bool queries = pieces(a.q, a.ldq, a.D, sizeof(T)) && pieces(a.dout, a.lddo, a.D, sizeof(T));
+    auto dq = keys ? k_attend_dq<T, DP, true> : k_attend_dq<T, DP, false>;
+    auto dkv = queries ? k_attend_dkv<T, DP, true> : k_attend_dkv<T, DP, false>;
+    TT_LAUNCH(nullptr, "k_attend_dq", a.s, dq, grid, block, 0, a.s, a);
     TT_LAUNCH_CHECK();
-    TT_LAUNCH(nullptr, "k_attend_dkv", a.s, (k_attend_dkv<T, DP>), dim3((unsigned)(tiles * a.kv)), block, 0, a.s, a);
+    TT_LAUNCH(nullptr, "k_attend_dkv", a.s, dkv, dim3((unsigned)(tiles * a.kv)), block, 0, a.s, a);
     TT_LAUNCH_CHECK();
     return TT_OK;
 }

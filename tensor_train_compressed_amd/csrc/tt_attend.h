@@ -185,27 +185,70 @@ __device__ __forceinline__ void load_row(RowPieces<T, DP>& f, const T* __restric
     }
 }
 
-// A tile's rows on their way to LDS through registers: thread t of THREADS holds slots
-// t, t + THREADS, ... Rows from `left` on, and pieces past D, are zeros.
-template <class T, int DP, int ROWS, int THREADS>
+// A tile's rows on their way to LDS; rows from `left` on, and pieces past D, become zeros.
+//
+// DMA: straight to LDS, 16 bytes a lane, for rows that start at whole pieces and D of whole
+// pieces. What lies past the rows or past D has an offset outside the buffer's
+// descriptor, for which the load delivers zeros. Otherwise through registers, read when
+// the loads are issued and stored once the tile is wanted.
+template <class T, int DP, int ROWS, int WAVES, bool DMA>
 struct TileLoad {
     typedef Tile<T, DP> L;
-    static constexpr int N = ROWS * L::SLOTS / THREADS;
-    static_assert(ROWS * L::SLOTS % THREADS == 0, "whole pieces a thread");
-    Piece r[N];
-    __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int left, int D) {
+    static constexpr int N = ROWS * L::SLOTS / (WAVES * 64);   // pieces of a lane
+    static_assert(ROWS * L::SLOTS % (WAVES * 64) == 0, "whole pieces a lane");
+    Piece r[DMA ? 1 : N];
+    uint32_t off[DMA ? N : 1];
+    int64_t ld;       // elements from row to row
+    int D, wave;
+    // slot i of this lane
+    __device__ __forceinline__ int slot(int i) const { return (wave * N + i) * 64 + (threadIdx.x & 63); }
+    __device__ __forceinline__ int row(int i) const { return slot(i) / L::SLOTS; }
+    __device__ __forceinline__ int piece(int i) const { return (slot(i) % L::SLOTS) ^ L::key(row(i)); }
+    __device__ __forceinline__ void init(int64_t ld_, int D_, int wave_) {
+        ld = ld_;
+        D = D_;
+        wave = wave_;
+        if constexpr (DMA) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int s = i * THREADS + threadIdx.x, row = s / L::SLOTS, piece = (s % L::SLOTS) ^ L::key(row);
-            const int e = piece * L::P;
-            r[i] = load_piece(p + row * ld + e, row < left ? max(0, min(L::P, D - e)) : 0);
+            for (int i = 0; i < N; ++i)
+                off[i] = piece(i) * L::P < D ? (uint32_t)((row(i) * ld + piece(i) * L::P) * sizeof(T)) : 0x80000000u;
+        }
+    }
+    __device__ __forceinline__ void issue(char* lds, const T* __restrict__ p, int left) {
+        if constexpr (DMA) {
+#ifdef __HIP_DEVICE_COMPILE__   // the descriptor's type is the device compiler's
+            const int64_t bytes = left * ld * (int64_t)sizeof(T);
+            const int records = left <= 0 ? 0 : bytes < 0x7FFFFFFF ? (int)bytes : 0x7FFFFFFF;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, records, 0x00020000);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * N + i) * 1024), 16, off[i], 0, 0, 0);
+#endif
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int e = piece(i) * L::P;
+                r[i] = load_piece(p + row(i) * ld + e, row(i) < left ? max(0, min(L::P, D - e)) : 0);
+            }
         }
     }
     __device__ __forceinline__ void store(char* lds) const {
+        if constexpr (!DMA) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<Piece*>(lds + (i * THREADS + threadIdx.x) * 16) = r[i];
+            for (int i = 0; i < N; ++i) *reinterpret_cast<Piece*>(lds + slot(i) * 16) = r[i];
+        }
     }
 };
+
+// Waits until this wave's loads to LDS have arrived and its LDS accesses are done, then
+// for the workgroup's other waves.
+__device__ __forceinline__ void landed_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
 // Where the n-th register of a lane's half lies in a block of 32 rows.
 __device__ __forceinline__ int block_row(int r) { return 8 * (r / 4) + 4 * ((threadIdx.x >> 5) & 1) + r % 4; }
