@@ -34,6 +34,8 @@ struct AttendArgs {
     int heads, kv, D, causal;
     float scale;
     float *lse, *delta;   // [heads][rows]
+    float* part;          // dk's, then dv's sums [splits][rows][kv * D]
+    int splits;
     hipStream_t s;
 };
 
@@ -54,7 +56,7 @@ enum Pass { FWD, DQ, DKV };
 template <class T, int DP, bool DMA, Pass PASS>
 constexpr int waves_of() {
     if (sizeof(T) == 4) return DP == 32 || (DP == 64 && DMA && PASS != DKV) ? 2 : 1;
-    if (PASS == DKV) return DP <= 64 || (DP == 96 && DMA) ? 2 : 1;
+    if (PASS == DKV) return DP <= 64 || DMA ? 2 : 1;
     return DP <= 96 || DMA ? 2 : 1;
 }
 
@@ -243,27 +245,43 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, DQ>())) void k_a
 }
 
 // dk and dv: a wave keeps 32 keys and goes over the queries of every head that reads them.
-template <class T, int DP, bool DMA>
-__global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, DKV>())) void k_attend_dkv(const AttendArgs a) {
+//
+// GROUPS = 2: two waves a SIMD, where the registers for keys, values and both sums are too
+// many for two (heads of more than 64): the second four waves have the first's keys and take
+// the other half of each tile of queries, keys and values are read from LDS, and the halves' sums
+// meet at the end.
+//
+// The (head, tile of queries) pairs of a tile of keys are split over a.splits workgroups where
+// there are too few of these to fill the chip; sums then go to the workspace and are joined by
+// k_attend_join.
+template <class T, int DP, bool DMA, int GROUPS>
+__global__ __launch_bounds__(GROUPS * kWaves * 64, (waves_of<T, DP, DMA, DKV>())) void k_attend_dkv(const AttendArgs a) {
     typedef Tile<T, DP> L;
-    constexpr int BM = tile_rows<T, DP>(), BLOCKS = BM / 32, BN = kWaves * kQueries;
+    constexpr int BM = tile_rows<T, DP>(), BLOCKS = BM / 32, BN = kWaves * kQueries, WAVES = GROUPS * kWaves;
+    static_assert(BLOCKS % GROUPS == 0, "a group takes whole blocks");
     __shared__ __align__(16) char sq0[BM * L::ROW], sd0[BM * L::ROW], sq1[BM * L::ROW], sd1[BM * L::ROW];
     __shared__ __align__(16) float st0[2 * BM], st1[2 * BM];   // a tile's lse (in powers of two), then its delta
+    __shared__ __align__(16) char sk[GROUPS == 2 ? BN * L::ROW : 16], sv[GROUPS == 2 ? BN * L::ROW : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kv = blockIdx.x % a.kv, group = a.heads / a.kv;
+    const int group = wave / kWaves, mine = wave % kWaves;   // of keys
+    int job = blockIdx.x;
+    const int kv = job % a.kv, heads = a.heads / a.kv;
+    job /= a.kv;
+    const int split = job % a.splits;
     Span sp;
-    if (!find_tile(a.offsets, a.seqs, a.rows, BN, blockIdx.x / a.kv, sp)) return;
-    const int first = sp.tile * BN, k0 = first + wave * kQueries, ki = k0 + (lane & 31);
+    if (!find_tile(a.offsets, a.seqs, a.rows, BN, job / a.splits, sp)) return;
+    const int first = sp.tile * BN, k0 = first + mine * kQueries, ki = k0 + (lane & 31);
     const bool there = ki < sp.len;
     const int64_t row = sp.first + ki, at = (int64_t)kv * a.D;
     const int begin = a.causal ? first / BM : 0, per = (sp.len + BM - 1) / BM - begin;   // tiles of queries a head
-    const int all = per * group;
-    TileLoad<T, DP, BM, kWaves, DMA> lq, ld;
+    const int all = per * heads, each = (all + a.splits - 1) / a.splits;
+    const int i0 = min(all, split * each), i1 = min(all, i0 + each);
+    TileLoad<T, DP, BM, WAVES, DMA> lq, ld;
     lq.init(a.ldq, a.D, wave);
     ld.init(a.lddo, a.D, wave);
     float stat = 0.f;   // of query threadIdx.x % BM of the tile
     auto issue = [&](int i, char* tq, char* td) TT_INLINE {
-        const int head = kv * group + i / per, q0 = (begin + i % per) * BM, left = sp.len - q0;
+        const int head = kv * heads + i / per, q0 = (begin + i % per) * BM, left = sp.len - q0;
         const int64_t r = sp.first + q0;
         lq.issue(tq, (const T*)a.q + r * a.ldq + (int64_t)head * a.D, left);
         ld.issue(td, (const T*)a.dout + r * a.lddo + (int64_t)head * a.D, left);
@@ -280,24 +298,38 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, DKV>())) void k_
         ld.store(td);
         if (threadIdx.x < 2 * BM) ts[threadIdx.x] = stat;
     };
-    issue(0, sq0, sd0);
     Piece fk[L::STEPS], fv[L::STEPS];
-    load_row<T, DP>(fk, (const T*)a.k + row * a.ldk + at, there, a.D);
-    load_row<T, DP>(fv, (const T*)a.v + row * a.ldv + at, there, a.D);
+    if constexpr (GROUPS == 2) {
+        TileLoad<T, DP, BN, WAVES, DMA> lk, lv;
+        lk.init(a.ldk, a.D, wave);
+        lv.init(a.ldv, a.D, wave);
+        lk.issue(sk, (const T*)a.k + (sp.first + first) * a.ldk + at, sp.len - first);
+        lv.issue(sv, (const T*)a.v + (sp.first + first) * a.ldv + at, sp.len - first);
+        lk.store(sk);
+        lv.store(sv);
+    } else {
+        load_row<T, DP>(fk, (const T*)a.k + row * a.ldk + at, there, a.D);
+        load_row<T, DP>(fv, (const T*)a.v + row * a.ldv + at, there, a.D);
+    }
+    if (i0 < i1) issue(i0, sq0, sd0);
     const float c = a.scale * kLog2e;
     floatx16 dk[DP / 32] = {}, dv[DP / 32] = {};
     store(sq0, sd0, st0);
     auto step = [&](int i, const char* sq, const char* sd, const float* st, char* tq, char* td, float* ts) TT_INLINE {
         landed_barrier();
-        if (i + 1 < all) issue(i + 1, tq, td);
+        if (i + 1 < i1) issue(i + 1, tq, td);
         const int q0 = (begin + i % per) * BM;
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-            const int first_q = q0 + 32 * b;
+        for (int n = 0; n < BLOCKS / GROUPS; ++n) {
+            const int b = GROUPS * n + group, first_q = q0 + 32 * b;
             if (first_q >= sp.len || (a.causal && first_q + 31 < k0)) continue;
             floatx16 s = {}, dp = {};
 #pragma unroll
             for (int x = 0; x < L::STEPS; ++x) {
+                if constexpr (GROUPS == 2) {
+                    fk[x] = L::row_piece(sk, mine * kQueries, x);
+                    fv[x] = L::row_piece(sv, mine * kQueries, x);
+                }
                 s = mma_rows<T>(L::row_piece(sq, 32 * b, x), fk[x], s);
                 dp = mma_rows<T>(L::row_piece(sd, 32 * b, x), fv[x], dp);
             }
@@ -329,15 +361,75 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<T, DP, DMA, DKV>())) void k_
 #pragma unroll
             for (int j = 0; j < DP / 32; ++j) dk[j] = mma_columns<T, DP>(sq, 32 * b, j, w, dk[j]);
         }
-        if (i + 1 < all) store(tq, td, ts);
+        if (i + 1 < i1) store(tq, td, ts);
     };
-    for (int i = 0; i < all; i += 2) {
+    for (int i = i0; i < i1; i += 2) {
         step(i, sq0, sd0, st0, sq1, sd1, st1);
-        if (i + 1 < all) step(i + 1, sq1, sd1, st1, sq0, sd0, st0);
+        if (i + 1 < i1) step(i + 1, sq1, sd1, st1, sq0, sd0, st0);
+    }
+    if constexpr (GROUPS == 2) {
+        // the first group takes the second's dk, the second the first's dv
+        static_assert(BM * L::ROW >= kWaves * 64 * 64, "room for 32 columns of the sums");
+        char* to = (group ? sq0 : sd0) + mine * 4096 + lane * 16;
+        const char* from = (group ? sd0 : sq0) + mine * 4096 + lane * 16;
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) {
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    reinterpret_cast<float*>(to + g * 1024)[e] = group ? dk[j][4 * g + e] : dv[j][4 * g + e];
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float f = reinterpret_cast<const float*>(from + g * 1024)[e];
+                    if (group) dv[j][4 * g + e] += f;
+                    else dk[j][4 * g + e] += f;
+                }
+        }
     }
     if (!there) return;
-    store_columns<T, DP>((T*)a.dk + row * a.lddk + at, dk, a.scale, a.D);
-    store_columns<T, DP>((T*)a.dv + row * a.lddv + at, dv, 1.f, a.D);
+    const bool has_dk = GROUPS == 1 || group == 0, has_dv = GROUPS == 1 || group == 1;
+    if (a.splits > 1) {
+        float* p = a.part + ((int64_t)split * a.rows + row) * a.kv * a.D + at;
+        if (has_dk) store_columns<float, DP>(p, dk, 1.f, a.D);
+        if (has_dv) store_columns<float, DP>(p + (int64_t)a.splits * a.rows * a.kv * a.D, dv, 1.f, a.D);
+    } else {
+        if (has_dk) store_columns<T, DP>((T*)a.dk + row * a.lddk + at, dk, a.scale, a.D);
+        if (has_dv) store_columns<T, DP>((T*)a.dv + row * a.lddv + at, dv, 1.f, a.D);
+    }
+}
+
+// dk (blockIdx.y = 0) and dv from the splits' sums, in their order.
+template <class T>
+__global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
+    const int N = a.kv * a.D, per = (N + 7) / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / per;
+    const int n = (int)(i - row * per) * 8, left = N - n;
+    if (row >= a.rows || row < a.offsets[0] || row >= a.offsets[a.seqs]) return;   // rows of no sequence stay
+    const bool second = blockIdx.y == 1;
+    const float* p = a.part + ((int64_t)second * a.splits * a.rows + row) * N + n;
+    float o[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const Raw8<float> f = load8n(p + (int64_t)s * a.rows * N, left, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += f.at(e);
+    }
+    if (!second)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= a.scale;
+    store8n((T*)(second ? a.dv : a.dk) + row * (second ? a.lddv : a.lddk) + n, o, left);
+}
+
+// Splits of dk's and dv's sums: as many as bring the workgroups to kMinGroups.
+constexpr int64_t kMinGroups = 512, kMaxSplits = 16;
+inline int64_t splits_of(int64_t rows, int64_t seqs, int64_t kv) {
+    const int64_t n = std::max<int64_t>(1, ((rows + kWaves * kQueries - 1) / (kWaves * kQueries) + seqs / 2) * kv);
+    return std::max<int64_t>(1, std::min(kMaxSplits, kMinGroups / n));
 }
 
 // Whether rows start at whole 16-byte pieces, and their heads are made of them.
@@ -355,13 +447,25 @@ tt_status attend_launch(const AttendArgs& a, bool backward) {
         TT_LAUNCH_CHECK();
         return TT_OK;
     }
-    const bool queries = pieces(a.q, a.ldq, a.D, sizeof(T)) && pieces(a.dout, a.lddo, a.D, sizeof(T));
+    const bool queries = pieces(a.q, a.ldq, a.D, sizeof(T)) && pieces(a.dout, a.lddo, a.D, sizeof(T)) &&
+                         (DP <= 64 || keys);
     auto dq = keys ? k_attend_dq<T, DP, true> : k_attend_dq<T, DP, false>;
-    auto dkv = queries ? k_attend_dkv<T, DP, true> : k_attend_dkv<T, DP, false>;
     TT_LAUNCH(nullptr, "k_attend_dq", a.s, dq, grid, block, 0, a.s, a);
     TT_LAUNCH_CHECK();
-    TT_LAUNCH(nullptr, "k_attend_dkv", a.s, dkv, dim3((unsigned)(tiles * a.kv)), block, 0, a.s, a);
+    const dim3 keys_grid((unsigned)(tiles * a.splits * a.kv));
+    if constexpr (sizeof(T) == 2 && DP > 64) {
+        auto dkv = queries ? k_attend_dkv<T, DP, true, 2> : k_attend_dkv<T, DP, false, 2>;
+        TT_LAUNCH(nullptr, "k_attend_dkv", a.s, dkv, keys_grid, dim3(2 * kWaves * 64), 0, a.s, a);
+    } else {
+        auto dkv = queries ? k_attend_dkv<T, DP, true, 1> : k_attend_dkv<T, DP, false, 1>;
+        TT_LAUNCH(nullptr, "k_attend_dkv", a.s, dkv, keys_grid, block, 0, a.s, a);
+    }
     TT_LAUNCH_CHECK();
+    if (a.splits > 1) {
+        const dim3 join(grid_for(a.rows * (((int64_t)a.kv * a.D + 7) / 8), 256), 2);
+        TT_LAUNCH(nullptr, "k_attend_join", a.s, (k_attend_join<T>), join, dim3(256), 0, a.s, a);
+        TT_LAUNCH_CHECK();
+    }
     return TT_OK;
 }
 
@@ -386,6 +490,10 @@ tt_status attend_sizes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv, i
     if (!dtype_ok(dtype) || rows < 0 || heads < 1 || kv < 1 || dim < 1 || heads % kv != 0) return TT_ERR_INVALID_ARG;
     if (dim > 128 || rows > INT32_MAX || heads > (int64_t(1) << 22)) return TT_ERR_UNSUPPORTED;
     return TT_OK;
+}
+
+inline size_t delta_bytes(int64_t rows, int64_t heads) {
+    return ((size_t)rows * heads * sizeof(float) + 255) & ~size_t(255);
 }
 
 // The arguments that every call takes.
@@ -417,7 +525,10 @@ using namespace tt;
 extern "C" size_t tt_emb_attend_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads,
                                                 int64_t dim) {
     if (attend_sizes(dtype, rows, heads, kv_heads, dim) != TT_OK) return 0;
-    return std::max<size_t>(256, ((size_t)rows * heads * sizeof(float) + 255) & ~size_t(255));
+    // delta; the splits' sums, of which fewer rows have at most kMinGroups workgroups'
+    const int64_t most = kMinGroups * kWaves * kQueries;
+    const int64_t sums = std::min(rows * kv_heads * kMaxSplits, most) * 2 * dim;
+    return delta_bytes(rows, heads) + std::max<size_t>(256, ((size_t)sums * sizeof(float) + 255) & ~size_t(255));
 }
 
 extern "C" tt_status tt_emb_attend_forward(int32_t dtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
@@ -457,5 +568,7 @@ extern "C" tt_status tt_emb_attend_backward(int32_t dtype, const void* q, int64_
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.lddq = lddq; a.lddk = lddk; a.lddv = lddv;
     a.delta = (float*)workspace;
+    a.part = (float*)((char*)workspace + delta_bytes(rows, heads));
+    a.splits = (int)splits_of(rows, seqs, kv_heads);
     return attend_by_type(dtype, a, true);
 }
