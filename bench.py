@@ -248,7 +248,7 @@ def hot_rows_step(args):
 
 # The dense operators' sources: no kernel of the measured path is in them.
 DENSE_SOURCES = ("tt_dense.h", "norm.hip", "gate.hip", "distill.hip",
-                 "tt_attend.h", "rotate.hip", "attend.hip", "paged.hip")
+                 "tt_attend.h", "attend.h", "rotate.hip", "attend.hip", "attend_dq.hip", "attend_dkv.hip", "paged.hip")
 
 
 def kernel_source_hash() -> str:

@@ -1,0 +1,117 @@
+// Shared by the kernels of attention over packed prompts (attend.hip, attend_dq.hip,
+// attend_dkv.hip).
+#pragma once
+
+#include "tt_attend.h"
+
+namespace tt {
+
+struct AttendArgs {
+    const void *q, *k, *v, *out, *dout;
+    int64_t ldq, ldk, ldv, ldo, lddo;
+    void *o, *dq, *dk, *dv;
+    int64_t lddq, lddk, lddv;
+    const int64_t* offsets;
+    int64_t seqs, rows;
+    int heads, kv, D, causal;
+    float scale;
+    float *lse, *delta;   // [heads][rows]
+    float* part;          // dk's, then dv's sums [splits][rows][kv * D]
+    int splits;
+    hipStream_t s;
+};
+
+// Lambdas of a kernel's loop are part of it, whatever their size.
+#define TT_INLINE __attribute__((always_inline))
+
+// f(0), .., f(N - 1) with constant arguments.
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<N, F, I + 1>(f);
+    }
+}
+
+// Fragments under way from LDS ahead of the product that takes them.
+constexpr int AHEAD = 4;
+
+constexpr int kQueries = 32;   // a wave's
+
+// Waves of a workgroup: four, or one where sequences are short. Histories of 20 rows on
+// average, 8192 rows in all, 4 heads of 32 fp32: WAVES_FIGURES
+constexpr int kWaves = 4;
+constexpr int64_t kShort = 64;   // rows a sequence, on average, up to which
+
+// Rows of a tile that goes through LDS.
+template <class T, int DP, int WAVES>
+constexpr int tile_rows() {
+    return WAVES > 1 && Tile<T, DP>::ROW <= 256 ? 64 : 32;
+}
+
+// Waves a SIMD is to hold: two where their registers allow it without spilling.
+enum Pass { FWD, DQ, DKV };
+template <class T, int DP, bool DMA, Pass PASS>
+constexpr int waves_of() {
+    if (sizeof(T) == 4) return DP == 32 || (DP == 64 && DMA && PASS != DKV) ? 2 : 1;
+    if (PASS == DKV) return DP <= 64 ? 2 : 1;
+    return DP <= 64 || DMA ? 2 : 1;
+}
+
+// The workgroup's tile and head: heads that share keys lie next to each other.
+struct Job {
+    int64_t tile;
+    int kv, head;
+};
+__device__ __forceinline__ Job job_of(const AttendArgs& a) {
+    const int i = blockIdx.x % a.heads, kv = i % a.kv;
+    return {(int64_t)(blockIdx.x / a.heads), kv, kv * (a.heads / a.kv) + i / a.kv};
+}
+
+// What weights are relative to, in powers of two: 2^(c s - it). Rows that see nothing have
+// none.
+__device__ __forceinline__ float log2_sum(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+// Whether rows start at whole 16-byte pieces, and their heads are made of them.
+inline bool pieces(const void* p, int64_t ld, int D, size_t size) {
+    return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && D * size % 16 == 0;
+}
+template <class T>
+bool keys_in_pieces(const AttendArgs& a) {
+    return pieces(a.k, a.ldk, a.D, sizeof(T)) && pieces(a.v, a.ldv, a.D, sizeof(T));
+}
+template <class T>
+bool queries_in_pieces(const AttendArgs& a) {
+    return pieces(a.q, a.ldq, a.D, sizeof(T)) && pieces(a.dout, a.lddo, a.D, sizeof(T));
+}
+inline bool short_sequences(const AttendArgs& a) { return a.rows <= kShort * a.seqs; }
+// Tiles of `size` rows that the sequences have at most.
+inline int64_t tiles_of(const AttendArgs& a, int64_t size) { return a.rows / size + a.seqs; }
+
+// f of the kernels' element type and of the heads' padded size.
+template <class T, class F>
+tt_status by_dim(const AttendArgs& a, F f) {
+    if (a.D <= 32) return f((T*)nullptr, std::integral_constant<int, 32>{});
+    if (a.D <= 64) return f((T*)nullptr, std::integral_constant<int, 64>{});
+    if (a.D <= 96) return f((T*)nullptr, std::integral_constant<int, 96>{});
+    return f((T*)nullptr, std::integral_constant<int, 128>{});
+}
+template <class F>
+tt_status by_type(int32_t dtype, const AttendArgs& a, F f) {
+    if (dtype == TT_F32) return by_dim<float>(a, f);
+    if (dtype == TT_BF16) return by_dim<bf16>(a, f);
+    return by_dim<f16>(a, f);
+}
+
+// The backward's two passes (attend_dq.hip, attend_dkv.hip): dq, with delta for the other; dk
+// and dv, whose sums may be split over workgroups.
+tt_status attend_dq(int32_t dtype, const AttendArgs& a);
+tt_status attend_dkv(int32_t dtype, const AttendArgs& a);
+// Splits, as many as bring the workgroups to kMinGroups.
+constexpr int64_t kMinGroups = 512, kMaxSplits = 16;
+inline int64_t splits_of(int64_t rows, int64_t seqs, int64_t kv) {
+    const int64_t n = std::max<int64_t>(1, ((rows + kWaves * kQueries - 1) / (kWaves * kQueries) + seqs / 2) * kv);
+    return std::max<int64_t>(1, std::min(kMaxSplits, kMinGroups / n));
+}
+
+}  // namespace tt

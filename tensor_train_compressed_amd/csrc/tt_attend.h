@@ -1,4 +1,4 @@
-// Shared by the attention kernels (attend.hip, paged.hip): 32 x 32 products on the
+// Shared by the attention kernels (attend*.hip, paged.hip): 32 x 32 products on the
 // matrix cores from tiles in LDS, whose rows are keys, values or queries of one head.
 //
 // A 16-byte piece of a row is what a lane takes at once. Products come in two forms:
@@ -84,6 +84,7 @@ __device__ __forceinline__ Piece load_piece(const T* __restrict__ p, int n) {
         __builtin_memcpy(&r, p, 16);
         return r;
     }
+    if (n <= 0) return r;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         if (i >= n) continue;

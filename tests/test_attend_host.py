@@ -267,6 +267,6 @@ def test_benchmark_counters_outlive_the_attention_sources(tmp_path, monkeypatch)
     first = bench.kernel_source_hash()
     shutil.copytree(bench.CSRC, tmp_path / "csrc")
     monkeypatch.setattr(bench, "CSRC", str(tmp_path / "csrc"))
-    for f in ("rotate.hip", "attend.hip", "paged.hip", "tt_attend.h"):
+    for f in ("rotate.hip", "attend.hip", "attend_dq.hip", "attend_dkv.hip", "paged.hip", "tt_attend.h", "attend.h"):
         (tmp_path / "csrc" / f).write_text("changed")
         assert bench.kernel_source_hash() == first, f
