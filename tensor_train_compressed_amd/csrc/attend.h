@@ -21,9 +21,6 @@ struct AttendArgs {
     hipStream_t s;
 };
 
-// Lambdas of a kernel's loop are part of it, whatever their size.
-#define TT_INLINE __attribute__((always_inline))
-
 // f(0), .., f(N - 1) with constant arguments.
 template <int N, class F, int I = 0>
 __device__ __forceinline__ void each(F f) {
@@ -107,11 +104,14 @@ tt_status by_type(int32_t dtype, const AttendArgs& a, F f) {
 // and dv, whose sums may be split over workgroups.
 tt_status attend_dq(int32_t dtype, const AttendArgs& a);
 tt_status attend_dkv(int32_t dtype, const AttendArgs& a);
-// Splits, as many as bring the workgroups to kMinGroups.
-constexpr int64_t kMinGroups = 512, kMaxSplits = 16;
+// Splits: where tiles of keys are fewer than would fill the chip twice, as many as bring them to
+// kGroups workgroups. 140 tiles of 64 wide heads, 8 to a key head (8192 rows in 8 sequences):
+// 510 us in one split, 185 in 3, 108 in 7 and 113 in 15, with 0, 6, 11 and 20 to join them; 512
+// tiles of 128 wide heads: 1230 in one, 1257 in two and 26 to join.
+constexpr int64_t kFull = 512, kGroups = 1024, kMaxSplits = 16;
 inline int64_t splits_of(int64_t rows, int64_t seqs, int64_t kv) {
     const int64_t n = std::max<int64_t>(1, ((rows + kWaves * kQueries - 1) / (kWaves * kQueries) + seqs / 2) * kv);
-    return std::max<int64_t>(1, std::min(kMaxSplits, kMinGroups / n));
+    return n >= kFull ? 1 : std::max<int64_t>(1, std::min(kMaxSplits, kGroups / n));
 }
 
 }  // namespace tt

@@ -190,8 +190,8 @@ using namespace tt;
 extern "C" size_t tt_emb_attend_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads,
                                                 int64_t dim) {
     if (attend_sizes(dtype, rows, heads, kv_heads, dim) != TT_OK) return 0;
-    // delta; the splits' sums, of which fewer rows have at most kMinGroups workgroups'
-    const int64_t most = kMinGroups * kWaves * kQueries;
+    // delta; the splits' sums, at most kGroups workgroups' at these and at fewer rows
+    const int64_t most = kGroups * kWaves * kQueries;
     const int64_t sums = std::min(rows * kv_heads * kMaxSplits, most) * 2 * dim;
     return delta_bytes(rows, heads) + std::max<size_t>(256, ((size_t)sums * sizeof(float) + 255) & ~size_t(255));
 }

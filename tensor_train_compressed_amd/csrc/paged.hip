@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kWaves = 4, kTokens = 32;           // tokens of a wave's tile
 constexpr int kHeads = 32;                        // heads of a workgroup at most
-constexpr int kMinChunk = 256;                    // tokens a workgroup takes, where there are that many
+constexpr int kMinChunk = 512;                    // tokens a workgroup takes, where there are that many
 
 struct PagedArgs {
     const void *q, *k, *v;
@@ -38,12 +38,20 @@ __device__ __forceinline__ int chunk_of(const PagedArgs& a, int len) {
     return max(kMinChunk, (n + kWaves * kTokens - 1) / (kWaves * kTokens) * (kWaves * kTokens));
 }
 
-template <class T, int DP>
-__global__ __launch_bounds__(kWaves * 64) void k_attend_paged(const PagedArgs a) {
+// DMA: keys and values go from memory straight to LDS, which needs whole, aligned 16-byte pieces;
+// a wave sends for the next tile's keys when this one's scores are formed, and for its values after
+// the outputs. Lanes without a piece (past D, or of tokens not seen) send for nothing: their
+// places are zeros from the start, or written so. Otherwise through registers.
+//
+// Two workgroups a CU: 8 waves with up to 16 KB under way each. A token over 32768 bf16 (8 key
+// heads of 128) took 40 us with one and registers that hold a tile under way.
+template <class T, int DP, bool DMA>
+__global__ __launch_bounds__(kWaves * 64, (DMA && sizeof(T) == 2) || DP == 32 ? 2 : 1) void k_attend_paged(const PagedArgs a) {
     typedef Tile<T, DP> L;
     constexpr int N = kTokens * L::SLOTS / 64, BYTES = kTokens * L::ROW;
-    static_assert(2 * BYTES >= kHeads * DP * 4, "room for a wave's sums");
-    __shared__ __align__(16) char tiles[kWaves][2 * BYTES];
+    constexpr int HALF = BYTES / (DP * 4);   // heads whose sums the place of a tile of keys takes
+    static_assert(2 * HALF >= kHeads, "room for a wave's sums");
+    __shared__ __align__(16) char tk[kWaves][BYTES], tv[kWaves][BYTES];
     __shared__ float sm_m[kWaves][kHeads], sm_l[kWaves][kHeads];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int b = blockIdx.x;
@@ -68,42 +76,86 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_paged(const PagedArgs a)
         const int64_t p = table[t / a.page];
         return p >= 0 && p < a.pages ? p * a.page + t % a.page : -1;
     };
-    Piece rk[N], rv[N];
-    uint32_t seen = 0;           // of the tile in rk and rv
-    auto load = [&](int t0) {
-        const int64_t row = row_of(t0);
+    char *sk = tk[wave], *sv = tv[wave];
+    auto slot_row = [&](int i) { return (i * 64 + lane) / L::SLOTS; };
+    auto slot_element = [&](int i) { return (((i * 64 + lane) % L::SLOTS) ^ L::key(slot_row(i))) * L::P; };
+    Piece rk[DMA ? 1 : N], rv[DMA ? 1 : N];
+    int64_t row = -1;            // of the tile that is sent for
+    uint32_t seen = 0;
+    auto find = [&](int t0) TT_INLINE {
+        row = row_of(t0);
         seen = (uint32_t)__ballot(row >= 0);
+    };
+    // Sends for the tile's keys or values.
+    auto send = [&](const void* from, char* lds, Piece (&r)[DMA ? 1 : N]) TT_INLINE {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = (i * 64 + lane) / L::SLOTS, piece = ((i * 64 + lane) % L::SLOTS) ^ L::key(r), e = piece * L::P;
-            const int64_t at = __shfl(row, r) * a.kv + kv;
-            const int n = seen >> r & 1 ? max(0, min(L::P, a.D - e)) : 0;
-            rk[i] = load_piece((const T*)a.k + at * a.D + e, n);
-            rv[i] = load_piece((const T*)a.v + at * a.D + e, n);
+            const int x = slot_row(i), e = slot_element(i);
+            const T* p = (const T*)from + (__shfl(row, x) * a.kv + kv) * a.D + e;
+            const bool there = seen >> x & 1;
+            if constexpr (DMA) {
+#ifdef __HIP_DEVICE_COMPILE__
+                if (there && e < a.D)
+                    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                                     (__attribute__((address_space(3))) void*)(lds + i * 1024), 16, 0, 0);
+                else
+                    *reinterpret_cast<Piece*>(lds + (i * 64 + lane) * 16) = Piece{0, 0, 0, 0};
+#endif
+            } else {
+                r[i] = load_piece(p, there ? max(0, min(L::P, a.D - e)) : 0);
+            }
         }
     };
-    char *sk = tiles[wave], *sv = sk + BYTES;
-    floatx16 o[DP / 32] = {};
-    Softmax<T> sm;
-    sm.init();
-    int t0 = begin + wave * kTokens;
-    if (t0 < end) load(t0);
-    for (; t0 < end; t0 += kWaves * kTokens) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+    // Until all that this wave has sent for is in LDS.
+    auto arrive = [&]() TT_INLINE {
+        if constexpr (DMA) {
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        } else {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            *reinterpret_cast<Piece*>(sk + (i * 64 + lane) * 16) = rk[i];
-            *reinterpret_cast<Piece*>(sv + (i * 64 + lane) * 16) = rv[i];
+            for (int i = 0; i < N; ++i) {
+                *reinterpret_cast<Piece*>(sk + (i * 64 + lane) * 16) = rk[i];
+                *reinterpret_cast<Piece*>(sv + (i * 64 + lane) * 16) = rv[i];
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+    // Until this wave's reads of a tile are done, which the next one's pieces are to overwrite.
+    auto taken = [&]() TT_INLINE {
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0)
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    };
+    floatx16 o[DP / 32] = {};
+    Softmax<T> sm;
+    sm.init();
+    int t0 = begin + wave * kTokens;
+    if (t0 < end) {
+        find(t0);
+        send(a.k, sk, rk);
+        send(a.v, sv, rv);
+    }
+    for (; t0 < end; t0 += kWaves * kTokens) {
+        arrive();
         const uint32_t here = seen;
-        if (t0 + kWaves * kTokens < end) load(t0 + kWaves * kTokens);
+        const int next = t0 + kWaves * kTokens;
+        if (next < end) find(next);
+        if (!DMA && next < end) {
+            send(a.k, sk, rk);
+            send(a.v, sv, rv);
+        }
         floatx16 s[1] = {};
 #pragma unroll
         for (int x = 0; x < L::STEPS; ++x) s[0] = mma_rows<T>(L::row_piece(sk, 0, x), fq[x], s[0]);
+        if (DMA && next < end) {
+            taken();
+            send(a.k, sk, rk);
+        }
         if (here != ~0u) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -117,6 +169,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_paged(const PagedArgs a)
         w.set(s[0]);
 #pragma unroll
         for (int j = 0; j < DP / 32; ++j) o[j] = mma_columns<T, DP>(sv, 0, j, w, o[j]);
+        if (DMA && next < end) {
+            taken();
+            send(a.v, sv, rv);
+        }
     }
 
     // the waves' sums, joined at the largest maximum; a head's row of sums lies in LDS in
@@ -135,7 +191,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_paged(const PagedArgs a)
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm_m[w][h]);
         const float f = Softmax<T>::moved(sm.m, top, c);
         if (h < heads) {
-            char* p = tiles[wave] + h * DP * 4;
+            char* p = h < HALF ? sk + h * DP * 4 : sv + (h - HALF) * DP * 4;
 #pragma unroll
             for (int j = 0; j < DP / 32; ++j)
 #pragma unroll
@@ -155,7 +211,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_paged(const PagedArgs a)
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             l += sm_l[w][n] * Softmax<T>::moved(sm_m[w][n], top, c);
-            const float4 x = *reinterpret_cast<const float4*>(tiles[w] + n * DP * 4 + ((d / 4) ^ (n & KEY)) * 16);
+            const char* p = n < HALF ? tk[w] + n * DP * 4 : tv[w] + (n - HALF) * DP * 4;
+            const float4 x = *reinterpret_cast<const float4*>(p + ((d / 4) ^ (n & KEY)) * 16);
             v[0] += x.x;
             v[1] += x.y;
             v[2] += x.z;
@@ -198,7 +255,6 @@ __global__ __launch_bounds__(256) void k_attend_paged_join(const PagedArgs a) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     if (y < ROWS) {
-#pragma unroll 4
         for (int i = y; i < used; i += ROWS) {
             const float2 ml = a.ml[at + i];
             const float f = Softmax<T>::moved(ml.x, top, c);
@@ -238,7 +294,9 @@ inline int64_t padded_dim(int64_t dim) { return (dim + 31) / 32 * 32; }
 template <class T, int DP>
 tt_status paged_launch(const PagedArgs& a) {
     const unsigned grid = (unsigned)((int64_t)a.seqs * a.splits * a.blocks * a.kv);
-    TT_LAUNCH(nullptr, "k_attend_paged", a.s, (k_attend_paged<T, DP>), dim3(grid), dim3(kWaves * 64), 0, a.s, a);
+    const bool whole = a.D * sizeof(T) % 16 == 0 && (((uintptr_t)a.k | (uintptr_t)a.v) & 15) == 0;
+    auto k = whole ? k_attend_paged<T, DP, true> : k_attend_paged<T, DP, false>;
+    TT_LAUNCH(nullptr, "k_attend_paged", a.s, k, dim3(grid), dim3(kWaves * 64), 0, a.s, a);
     TT_LAUNCH_CHECK();
     if (a.splits > 1) {
         TT_LAUNCH(nullptr, "k_attend_paged_join", a.s, (k_attend_paged_join<T, DP>), dim3(a.seqs * a.heads), dim3(256), 0,

@@ -24,6 +24,9 @@ typedef uint32_t Piece __attribute__((ext_vector_type(4)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 
+// Lambdas of a kernel's loop are part of it, whatever their size.
+#define TT_INLINE __attribute__((always_inline))
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // [m c], rounded before anything else is done with it: sums relative to it stay exact.
