@@ -11,7 +11,8 @@
 // turns in fp64 (position freq / 2 pi less its whole turns), so that positions far
 // along keep the digits of their angle, and go to sine and cosine in fp32.
 //
-// Bound by memory: a head is read once and stays in registers. A head is cut into
+// Bound by memory (forward: 8192 rows of 32 and 8 heads of 128 bf16 in 31 us, 5.4 TB/s): a head is
+// read once and stays in registers. A head is cut into
 // chunks of 8 pairs, one a lane, so that both of a pair are the lane's own whatever
 // the pairing and the rotated part; what is not rotated goes in chunks of 16. A wave
 // takes one row and goes over its heads 64 / lanes-a-head at a time, with the
@@ -36,7 +37,8 @@ struct RotateArgs {
     int64_t ldoq, ldok;
     const int64_t* slots;             // append: a row's place in the cache, ok and ov
     int64_t nslots;
-    float* part;                      // backward: [groups][2][dim]
+    float* part;                      // backward: [q_groups + k_groups][dim]
+    int q_groups, k_groups;
     void *dwq, *dwk;
     int64_t rows;
     int heads, kv, dim, half;         // half: pairs
@@ -206,114 +208,122 @@ __global__ __launch_bounds__(kThreads) void k_rotate(const RotateArgs a) {
     }
 }
 
-// Backward: a wave takes whole rows, `gridDim.x` groups of four apart, and sums dw
-// of its heads in registers.
+// Backward: the first q_groups workgroups take queries, the others keys, so that a wave holds one
+// weight and one sum. A wave takes whole rows, and sums dw of its heads in registers. 8192 rows
+// of 32 and 8 heads of 128 bf16: 57 us, 4.4 TB/s; the same with the next round's pieces fetched
+// ahead (219 registers) or both weights in a wave (170), 66 with registers for a fourth wave a SIMD.
 template <class T, class W, int LANES>
 __global__ __launch_bounds__(kThreads) void k_rotate_back(const RotateArgs a) {
     constexpr int HEADS = 64 / LANES;
     __shared__ float2 sm[kWaves][kMaxDim / 2];
-    __shared__ float sum[kWaves][2][LANES * 16];
+    __shared__ float sum[kWaves][LANES * 16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool is_q = (int)blockIdx.x < a.q_groups;
+    const int group = is_q ? blockIdx.x : blockIdx.x - a.q_groups, groups = is_q ? a.q_groups : a.k_groups;
+    const int heads = is_q ? a.heads : a.kv;
+    const T *x0 = (const T*)(is_q ? a.q : a.k), *dy0 = (const T*)(is_q ? a.dyq : a.dyk);
+    T* dx0 = (T*)(is_q ? a.oq : a.ok);
+    const int64_t ldx = is_q ? a.ldq : a.ldk, lddy = is_q ? a.lddyq : a.lddyk, lddx = is_q ? a.ldoq : a.ldok;
     const Chunk k = chunk_of(a, lane % LANES);
-    float wq[16], wk[16], dwq[16] = {}, dwk[16] = {};
-    load_chunk((const W*)a.wq, k, wq);
-    load_chunk((const W*)a.wk, k, wk);
+    float w[16], dw[16] = {};
+    load_chunk((const W*)(is_q ? a.wq : a.wk), k, w);
     const float inv_dim = 1.f / (float)a.dim;
-    const int all = a.heads + a.kv;
-    for (int64_t row = (int64_t)blockIdx.x * kWaves + wave; row < a.rows; row += (int64_t)gridDim.x * kWaves) {
+    for (int64_t row = (int64_t)group * kWaves + wave; row < a.rows; row += (int64_t)groups * kWaves) {
         float c[8], s[8];
         turns_of(a, row, k, sm[wave], c, s);
-        for (int h = lane / LANES; h < all; h += HEADS) {
-            const bool is_q = h < a.heads;
-            const int hk = h - a.heads;
-            const T* src = is_q ? (const T*)a.q + row * a.ldq + (int64_t)h * a.dim
-                                : (const T*)a.k + row * a.ldk + (int64_t)hk * a.dim;
-            const T* dy = is_q ? (const T*)a.dyq + row * a.lddyq + (int64_t)h * a.dim
-                               : (const T*)a.dyk + row * a.lddyk + (int64_t)hk * a.dim;
-            T* dst = is_q ? (T*)a.oq + row * a.ldoq + (int64_t)h * a.dim
-                          : (T*)a.ok + row * a.ldok + (int64_t)hk * a.dim;
+        for (int h = lane / LANES; h < heads; h += HEADS) {
+            const int64_t at = (int64_t)h * a.dim;
             float x[16], g[16];
-            load_chunk(src, k, x);
-            load_chunk(dy, k, g);
+            load_chunk(x0 + row * ldx + at, k, x);
+            load_chunk(dy0 + row * lddy + at, k, g);
             const float rstd = rstd_of<LANES>(x, inv_dim, a.eps);
             turn(g, k, c, s, a.neighbours, -1.f);
             float tn = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 x[e] *= rstd;             // n
-                const float d = g[e] * x[e];
-                if (is_q) dwq[e] += d;
-                else dwk[e] += d;
-                g[e] *= is_q ? wq[e] : wk[e];
+                dw[e] = fmaf(g[e], x[e], dw[e]);
+                g[e] *= w[e];
                 tn = fmaf(g[e], x[e], tn);
             }
             tn = lanes_sum<LANES>(tn) * inv_dim;
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = rstd * (g[e] - x[e] * tn);
-            store_chunk(dst, k, x);
+            store_chunk(dx0 + row * lddx + at, k, x);
         }
     }
     // the heads of a round lie LANES lanes apart
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
 #pragma unroll
-        for (int m = LANES; m < 64; m *= 2) {
-            dwq[e] += __shfl_xor(dwq[e], m);
-            dwk[e] += __shfl_xor(dwk[e], m);
-        }
-        if (lane < LANES) {
-            sum[wave][0][lane * 16 + e] = dwq[e];
-            sum[wave][1][lane * 16 + e] = dwk[e];
-        }
+        for (int m = LANES; m < 64; m *= 2) dw[e] += __shfl_xor(dw[e], m);
+        if (lane < LANES) sum[wave][lane * 16 + e] = dw[e];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * LANES * 16; i += kThreads) {
-        const int z = i / (LANES * 16), j = i % (LANES * 16), e = j % 16;
+    for (int j = threadIdx.x; j < LANES * 16; j += kThreads) {
+        const int e = j % 16;
         const Chunk m = chunk_of(a, j / 16);
         const int at = e < 8 ? m.o0 + e : m.o1 + e - 8;
         if (e < 8 ? e >= m.n0 : e - 8 >= m.n1) continue;
         float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) t += sum[w][z][j];
-        a.part[((int64_t)blockIdx.x * 2 + z) * a.dim + at] = t;
+        for (int v = 0; v < kWaves; ++v) t += sum[v][j];
+        a.part[(int64_t)blockIdx.x * a.dim + at] = t;
     }
 }
 
-// dw from the groups' sums, in their order: a workgroup takes 16 of the 2 dim elements.
+// dw from the groups' sums, in their order: a workgroup takes 16 elements of one weight
+// (blockIdx.y), 64 groups at a time.
+constexpr int kJoinRows = 64;
 template <class W>
-__global__ __launch_bounds__(kThreads) void k_rotate_join(const float* __restrict__ part, int groups, int dim,
-                                                          W* __restrict__ dwq, W* __restrict__ dwk) {
-    __shared__ float sm[16][17];
+__global__ __launch_bounds__(16 * kJoinRows) void k_rotate_join(const float* __restrict__ part, int q_groups,
+                                                                int k_groups, int dim, W* __restrict__ dwq,
+                                                                W* __restrict__ dwk) {
+    __shared__ float sm[kJoinRows][17];
     const int x = threadIdx.x % 16, y = threadIdx.x / 16, i = blockIdx.x * 16 + x;
+    const int groups = blockIdx.y ? k_groups : q_groups;
+    const float* p = part + (blockIdx.y ? (int64_t)q_groups * dim : 0) + i;
     float t = 0.f;
-    if (i < 2 * dim)
-        for (int g = y; g < groups; g += 16) t += part[(int64_t)g * 2 * dim + i];
+    if (i < dim) {
+#pragma unroll 4
+        for (int g = y; g < groups; g += kJoinRows) t += p[(int64_t)g * dim];
+    }
     sm[y][x] = t;
     __syncthreads();
-    if (y > 0 || i >= 2 * dim) return;
+    if (y > 0 || i >= dim) return;
     t = 0.f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) t += sm[j][x];
-    if (i < dim) dwq[i] = (W)t;
-    else dwk[i - dim] = (W)t;
+    for (int j = 0; j < kJoinRows; ++j) t += sm[j][x];
+    (blockIdx.y ? dwk : dwq)[i] = (W)t;
 }
 
-// Workgroups of the backward: up to four a CU.
-constexpr int64_t kMaxGroups = 1024;
-inline int64_t back_groups(int64_t rows) { return std::min<int64_t>(kMaxGroups, (rows + kWaves - 1) / kWaves); }
+// Workgroups of the backward, shared by queries and keys as their heads are: the three a CU that
+// registers allow (768: 57 us; 512: 66; 1024: 63).
+constexpr int64_t kMaxGroups = 768;
+struct BackGroups {
+    int64_t q, k;
+};
+inline BackGroups back_groups(int64_t rows, int64_t heads, int64_t kv) {
+    const int64_t most = (rows + kWaves - 1) / kWaves;
+    const int64_t q = std::max<int64_t>(1, kMaxGroups * heads / (heads + kv));
+    return {std::min(most, q), std::min(most, std::max<int64_t>(1, kMaxGroups - q))};
+}
 
 template <class T, class W, int LANES>
 tt_status rotate_launch(RotateArgs a, bool backward) {
     const int rounds = (a.heads + a.kv * (a.slots ? 2 : 1) + 64 / LANES - 1) / (64 / LANES);
     const dim3 block(kThreads);
     if (backward) {
-        const int groups = (int)back_groups(a.rows);
-        if (groups > 0) {
-            TT_LAUNCH(nullptr, "k_rotate_back", a.s, (k_rotate_back<T, W, LANES>), dim3(groups), block, 0, a.s, a);
+        const BackGroups g = back_groups(a.rows, a.heads, a.kv);
+        a.q_groups = (int)g.q;
+        a.k_groups = (int)g.k;
+        if (a.rows > 0) {
+            TT_LAUNCH(nullptr, "k_rotate_back", a.s, (k_rotate_back<T, W, LANES>), dim3(a.q_groups + a.k_groups), block, 0,
+                      a.s, a);
             TT_LAUNCH_CHECK();
         }
-        TT_LAUNCH(nullptr, "k_rotate_join", a.s, (k_rotate_join<W>), dim3((2 * a.dim + 15) / 16), block, 0, a.s, a.part,
-                  groups, a.dim, (W*)a.dwq, (W*)a.dwk);
+        TT_LAUNCH(nullptr, "k_rotate_join", a.s, (k_rotate_join<W>), dim3((a.dim + 15) / 16, 2), dim3(16 * kJoinRows), 0,
+                  a.s, a.part, a.q_groups, a.k_groups, a.dim, (W*)a.dwq, (W*)a.dwk);
         TT_LAUNCH_CHECK();
         return TT_OK;
     }
@@ -383,7 +393,8 @@ using namespace tt;
 extern "C" size_t tt_emb_rotate_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads,
                                                 int64_t dim) {
     if (rotate_sizes(dtype, rows, heads, kv_heads, dim) != TT_OK) return 0;
-    return std::max<size_t>(256, ((size_t)back_groups(rows) * 2 * dim * sizeof(float) + 255) & ~size_t(255));
+    const BackGroups g = back_groups(rows, heads, kv_heads);
+    return std::max<size_t>(256, ((size_t)(g.q + g.k) * dim * sizeof(float) + 255) & ~size_t(255));
 }
 
 extern "C" tt_status tt_emb_rotate_forward(int32_t dtype, int32_t wdtype, const void* q, int64_t ldq, const void* k,
