@@ -492,7 +492,8 @@ tt_status tt_emb_rotate_backward(int32_t dtype, int32_t wdtype, const void* q, i
  *   s_ij = scale q_i . k_j,  out_i = sum_j softmax_j(s_ij) v_j
  * Rows of no sequence (before the first, behind the last) are neither read nor
  * written. A score that is -inf counts as not seen; a row that sees nothing
- * gives 0.
+ * gives 0. An infinity or NaN in a row may reach every row of its sequence (a
+ * weight of 0 times it), and no other's.
  *   lse  float[heads][rows], log sum_j e^(s_ij), what the backward needs; NULL
  *        when serving
  * With 16-bit types the weights e^(s - max) are rounded to dtype before they
@@ -501,7 +502,7 @@ tt_status tt_emb_rotate_backward(int32_t dtype, int32_t wdtype, const void* q, i
  * range. Offsets that decrease or lie outside the rows leave the outputs
  * unspecified. The workspace is the backward's.
  * Limits: 0 < scale < inf; dim <= 128, rows < 2^31, row strides < 2^22,
- * (rows / 32 + seqs) * heads <= 2^24. */
+ * (rows / 32 + seqs) * heads <= 2^22. */
 size_t tt_emb_attend_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim);
 tt_status tt_emb_attend_forward(int32_t dtype, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                                 int64_t ldv, const int64_t* offsets, int64_t seqs, void* out, int64_t ldo, float* lse,

@@ -171,7 +171,8 @@ tt_status attend_args(AttendArgs& a, int32_t dtype, const void* q, int64_t ldq, 
     if (ldq < heads * dim || ldk < kv * dim || ldv < kv * dim) return TT_ERR_INVALID_ARG;
     if (rows > 0 && seqs > 0 && (!q || !k || !v || !offsets)) return TT_ERR_INVALID_ARG;
     if (ldq > kMaxLd || ldk > kMaxLd || ldv > kMaxLd || seqs > INT32_MAX) return TT_ERR_UNSUPPORTED;
-    if ((rows / kQueries + seqs) * heads > int64_t(1) << 24) return TT_ERR_UNSUPPORTED;
+    // (a launch's threads, 512 a workgroup at most, must stay below 2^32)
+    if ((rows / kQueries + seqs) * heads > int64_t(1) << 22) return TT_ERR_UNSUPPORTED;
     a = AttendArgs{};
     a.q = q; a.k = k; a.v = v;
     a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;

@@ -231,54 +231,71 @@ __global__ __launch_bounds__(kWaves * 64, (DMA && sizeof(T) == 2) || DP == 32 ? 
     }
 }
 
-// Joins the workgroups of a sequence's head.
+// Joins the workgroups of a sequence's head: their factors first, then their sums, several
+// under way.
+constexpr int64_t kMaxSplits = 512;   // of a sequence
 template <class T, int DP>
 __global__ __launch_bounds__(256) void k_attend_paged_join(const PagedArgs a) {
-    constexpr int LANES = DP / 4, ROWS = 256 / LANES;   // splits at a time
+    constexpr int LANES = DP / 4, ROWS = 256 / LANES, DEEP = 4;   // ROWS splits at a time
     __shared__ float4 sm_v[256];
-    __shared__ float sm_m[256], sm_l[256];
+    __shared__ float factor[kMaxSplits], sm[2][4];
     const int seq = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     const int len = length_of(a, seq), chunk = chunk_of(a, len), used = max(1, (len + chunk - 1) / chunk);
     if (used == 1) return;
     const int64_t at = (int64_t)blockIdx.x * a.splits;
     const float c = a.scale * kLog2e;
-    const int x = threadIdx.x % LANES, y = threadIdx.x / LANES;
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < used; i += 256) top = fmaxf(top, a.ml[at + i].x);
-    sm_m[threadIdx.x] = top;
-    __syncthreads();
-    for (int i = 128; i > 0; i /= 2) {
-        if ((int)threadIdx.x < i) sm_m[threadIdx.x] = fmaxf(sm_m[threadIdx.x], sm_m[threadIdx.x + i]);
-        __syncthreads();
+    const int x = threadIdx.x % LANES, y = threadIdx.x / LANES, wave = threadIdx.x >> 6;
+    static_assert(kMaxSplits == 2 * 256, "two splits a thread");
+    float2 ml[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = threadIdx.x + u * 256;
+        ml[u] = i < used ? a.ml[at + i] : make_float2(-INFINITY, 0.f);
     }
-    top = sm_m[0];
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = lanes_max<64>(fmaxf(ml[0].x, ml[1].x));
+    if ((threadIdx.x & 63) == 0) sm[0][wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(sm[0][0], sm[0][1]), fmaxf(sm[0][2], sm[0][3]));
     float l = 0.f;
-    if (y < ROWS) {
-        for (int i = y; i < used; i += ROWS) {
-            const float2 ml = a.ml[at + i];
-            const float f = Softmax<T>::moved(ml.x, top, c);
-            const float4 o = *reinterpret_cast<const float4*>(a.part + (at + i) * DP + x * 4);
-            v.x = fmaf(o.x, f, v.x);
-            v.y = fmaf(o.y, f, v.y);
-            v.z = fmaf(o.z, f, v.z);
-            v.w = fmaf(o.w, f, v.w);
-            l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const float f = Softmax<T>::moved(ml[u].x, top, c);
+        factor[threadIdx.x + u * 256] = f;
+        l += ml[u].y * f;
+    }
+    l = lanes_sum<64>(l);
+    if ((threadIdx.x & 63) == 0) sm[1][wave] = l;
+    __syncthreads();
+    l = (sm[1][0] + sm[1][1]) + (sm[1][2] + sm[1][3]);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = y; y < ROWS && i0 < used; i0 += DEEP * ROWS) {
+        float4 o[DEEP];
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) {
+            const int i = i0 + u * ROWS;
+            o[u] = i < used ? *reinterpret_cast<const float4*>(a.part + (at + i) * DP + x * 4)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) {
+            const int i = i0 + u * ROWS;
+            const float f = i < used ? factor[i] : 0.f;
+            v.x = fmaf(o[u].x, f, v.x);
+            v.y = fmaf(o[u].y, f, v.y);
+            v.z = fmaf(o[u].z, f, v.z);
+            v.w = fmaf(o[u].w, f, v.w);
         }
     }
     sm_v[threadIdx.x] = v;
-    sm_l[threadIdx.x] = l;
     __syncthreads();
     if (threadIdx.x >= LANES) return;
     float r[4] = {};
-    l = 0.f;
     for (int i = 0; i < ROWS; ++i) {
         const float4 o = sm_v[i * LANES + x];
         r[0] += o.x;
         r[1] += o.y;
         r[2] += o.z;
         r[3] += o.w;
-        l += sm_l[i * LANES + x];
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -286,8 +303,8 @@ __global__ __launch_bounds__(256) void k_attend_paged_join(const PagedArgs a) {
     store4n((T*)a.out + seq * a.ldo + (int64_t)head * a.D + x * 4, r, a.D - x * 4);
 }
 
-// Workgroups that a call is split to reach, and the splits of a sequence at most.
-constexpr int64_t kGroups = 2048, kMaxSplits = 512;
+// Workgroups that a call is split to reach.
+constexpr int64_t kGroups = 2048;
 
 inline int64_t padded_dim(int64_t dim) { return (dim + 31) / 32 * 32; }
 
