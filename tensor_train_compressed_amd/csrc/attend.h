@@ -30,15 +30,20 @@ __device__ __forceinline__ void each(F f) {
     }
 }
 
-// Fragments under way from LDS ahead of the product that takes them.
+// Fragments under way from LDS ahead of the product that takes them (read right before it: forward
+// of the long prompt below 577 us instead of 555).
 constexpr int AHEAD = 4;
 
 constexpr int kQueries = 32;   // a wave's
 
-// Waves of a workgroup: four, or one where sequences are short. Histories of 20 rows on
-// average, 8192 rows in all, 4 heads of 32 fp32: WAVES_FIGURES
+// Waves of a workgroup: four, or one where sequences are short (and rows in whole pieces), whose
+// tiles the other three would have no part in. 16384 rows in sequences of equal length, us of the
+// forward and of the backward, one wave and four:
+//   4 heads of 32 fp32            20 rows 17 44, 50 120;  64 rows 15 44, 20 59;  128 rows 21 57, 28 86;  192 rows 24 66, 26 80
+//   16 and 4 heads of 64 bf16     20 rows 49 99, 129 214; 64 rows 46 97, 55 112; 128 rows 46 104, 85 179; 192 rows 48 116, 56 130
+//   32 and 8 heads of 128 bf16    20 rows 206 438, 333 905; 64 rows 174 388, 181 447; 128 rows 184 425, 174 505; 192 rows 192 467, 186 448
 constexpr int kWaves = 4;
-constexpr int64_t kShort = 64;   // rows a sequence, on average, up to which
+constexpr int64_t kShort = 128;   // rows a sequence, on average, up to which
 
 // Rows of a tile that goes through LDS.
 template <class T, int DP, int WAVES>
@@ -46,7 +51,9 @@ constexpr int tile_rows() {
     return WAVES > 1 && Tile<T, DP>::ROW <= 256 ? 64 : 32;
 }
 
-// Waves a SIMD is to hold: two where their registers allow it without spilling.
+// Waves a SIMD is to hold: two where their registers allow it without spilling (loads from where
+// registers were spilled to wait for all that is under way to LDS, which took a kernel from 560 to
+// 1230 us).
 enum Pass { FWD, DQ, DKV };
 template <class T, int DP, bool DMA, Pass PASS>
 constexpr int waves_of() {

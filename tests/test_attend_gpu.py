@@ -206,6 +206,21 @@ def test_attend_long(dt, dim):
     check_attend(dt, [1000, 523], 2, 1, dim)
 
 
+@TYPES
+@pytest.mark.parametrize("dim", [32, 64, 128])
+def test_attend_many_heads(dt, dim):
+    """As many tiles of keys as fill the chip: sums that are not split."""
+    check_attend(dt, [600, 424], 64, 64, dim)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[128, 128, 128], [128, 130, 128], [255, 256, 257, 258]])
+def test_attend_around_the_kernels_choices(dt, lengths):
+    """Sequences around what one wave takes, and around what forms delta from the weights."""
+    check_attend(dt, lengths, 4, 2, 64)
+    check_attend(dt, lengths, 2, 2, 128, causal=False)
+
+
 def test_attend_many_sequences():
     """More than 64, and more than 64 x 64, sequences to look through; most of them empty."""
     check_attend(BF16, [3, 0, 5, 1] * 60, 2, 1, 32)

@@ -92,9 +92,11 @@ def check_attend_shared(c):
 
 def test_attend_refusals():
     head = dict(dtype=0, q=A, ldq=32, k=A, ldk=16, v=A, ldv=16, offsets=A, seqs=1)
-    c = Call("tt_emb_attend_forward", **head, out=A, ldo=32, lse=None, **SIZES, causal=1, scale=F(1.0))
+    c = Call("tt_emb_attend_forward", **head, out=A, ldo=64, lse=None, **SIZES, causal=1, scale=F(1.0))
     check_attend_shared(c)
     c.refuse(INVALID, out=None, ldo=31)
+    assert c(rows=1 << 25, heads=8, kv=2, ldq=64) == UNSUPPORTED        # more threads than a launch takes
+    assert c(seqs=(1 << 20) + 1) == UNSUPPORTED
     assert c(rows=0, q=None, k=None, v=None, offsets=None, out=None) == OK and c(seqs=0) == OK
     c = Call("tt_emb_attend_backward", **head, out=A, ldo=32, lse=A, dout=A, lddo=32, dq=A, lddq=32, dk=A, lddk=16, dv=A,
              lddv=16, **SIZES, causal=1, scale=F(1.0), ws=A, n=1 << 20)
