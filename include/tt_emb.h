@@ -501,7 +501,7 @@ tt_status tt_emb_rotate_backward(int32_t dtype, int32_t wdtype, const void* q, i
  * before they meet the other factors; with TT_F16 the latter must lie in its
  * range. Offsets that decrease or lie outside the rows leave the outputs
  * unspecified. The workspace is the backward's.
- * Limits: 0 < scale < inf; dim <= 128, rows < 2^31, row strides < 2^22,
+ * Limits: 0 < scale < 2e38; dim <= 128, rows < 2^31, row strides < 2^22,
  * (rows / 32 + seqs) * heads <= 2^22. */
 size_t tt_emb_attend_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim);
 tt_status tt_emb_attend_forward(int32_t dtype, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
@@ -524,8 +524,8 @@ tt_status tt_emb_attend_backward(int32_t dtype, const void* q, int64_t ldq, cons
  * that sees nothing gives 0.
  *   table  int32, most_pages entries a sequence, ldt apart
  * The workspace serves any lengths, and fewer sequences.
- * Limits: 0 < scale < inf; dim <= 128, heads / kv_heads <= 256,
- * most_pages * page_size < 2^31, seqs * heads <= 2^20. */
+ * Limits: 0 < scale < 2e38; dim <= 128, heads / kv_heads <= 256,
+ * most_pages * page_size <= 2^30, seqs * heads <= 2^20. */
 size_t tt_emb_attend_paged_workspace_bytes(int32_t dtype, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t dim);
 tt_status tt_emb_attend_paged(int32_t dtype, const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
                               int64_t pages, int64_t page_size, const int32_t* table, int64_t ldt, int64_t most_pages,

@@ -175,7 +175,7 @@ tt_status attend_args(AttendArgs& a, int32_t dtype, const void* q, int64_t ldq, 
                       int64_t kv, int64_t dim, int32_t causal, float scale, void* stream) {
     const tt_status st = attend_sizes(dtype, rows, heads, kv, dim);
     if (st != TT_OK) return st;
-    if (seqs < 0 || !(scale > 0.f && scale < INFINITY)) return TT_ERR_INVALID_ARG;
+    if (seqs < 0 || !scale_ok(scale)) return TT_ERR_INVALID_ARG;
     if (ldq < heads * dim || ldk < kv * dim || ldv < kv * dim) return TT_ERR_INVALID_ARG;
     if (rows > 0 && seqs > 0 && (!q || !k || !v || !offsets)) return TT_ERR_INVALID_ARG;
     if (ldq > kMaxLd || ldk > kMaxLd || ldv > kMaxLd || seqs > INT32_MAX) return TT_ERR_UNSUPPORTED;

@@ -198,6 +198,7 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
         if (i + 1 < i1) step(i + 1, sq1, sd1, st1, sq0, sd0, st0);
     }
     if constexpr (GROUPS == 2) {
+        landed_barrier();   // (keys and values of a split without queries may be under way)
         // the first group takes the second's dk, the second the first's dv
         static_assert(BM * L::ROW >= KEYS * 64 * 64, "room for 32 columns of the sums");
         char* to = (group ? sq0 : sd0) + mine * 4096 + lane * 16;

@@ -307,6 +307,8 @@ __global__ __launch_bounds__(256) void k_attend_paged_join(const PagedArgs a) {
     store4n((T*)a.out + seq * a.ldo + (int64_t)head * a.D + x * 4, r, a.D - x * 4);
 }
 
+// Tokens of a sequence at most: counts past its end stay within 32 bits.
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
 // Workgroups that a call is split to reach.
 constexpr int64_t kGroups = 2048;
 
@@ -366,12 +368,12 @@ extern "C" tt_status tt_emb_attend_paged(int32_t dtype, const void* q, int64_t l
                                          float scale, void* workspace, size_t workspace_bytes, void* stream) {
     const tt_status st = paged_sizes(dtype, seqs, heads, kv_heads, dim);
     if (st != TT_OK) return st;
-    if (pages < 0 || page_size < 1 || most_pages < 0 || ldt < most_pages || !(scale > 0.f && scale < INFINITY))
+    if (pages < 0 || page_size < 1 || most_pages < 0 || ldt < most_pages || !scale_ok(scale))
         return TT_ERR_INVALID_ARG;
     if (ldq < heads * dim || ldo < heads * dim) return TT_ERR_INVALID_ARG;
     if (seqs > 0 && (!q || !out || !lengths || (most_pages > 0 && !table) || (pages > 0 && (!k_pages || !v_pages))))
         return TT_ERR_INVALID_ARG;
-    if (page_size > INT32_MAX || most_pages > INT32_MAX || most_pages * page_size > INT32_MAX || pages > INT32_MAX)
+    if (page_size > INT32_MAX || most_pages > INT32_MAX || most_pages * page_size > kMaxTokens || pages > INT32_MAX)
         return TT_ERR_UNSUPPORTED;
     if (!workspace || ((uintptr_t)workspace & 255) != 0) return TT_ERR_INVALID_ARG;
     if (workspace_bytes < tt_emb_attend_paged_workspace_bytes(dtype, seqs, heads, kv_heads, dim))

@@ -27,6 +27,9 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 // Lambdas of a kernel's loop are part of it, whatever their size.
 #define TT_INLINE __attribute__((always_inline))
 
+// A scale whose product with log2 e is finite, too.
+inline bool scale_ok(float scale) { return scale > 0.f && scale < 2e38f; }
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // [m c], rounded before anything else is done with it: sums relative to it stay exact.

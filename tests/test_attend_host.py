@@ -84,7 +84,7 @@ def test_rotate_backward_refusals():
 
 def check_attend_shared(c):
     c.refuse(INVALID, dtype=[3, -1], q=None, k=None, v=None, offsets=None, ldq=31, ldk=15, ldv=15, seqs=-1, rows=-1,
-             heads=[0, 3], kv=0, dim=0, scale=[F(0.0), F(-1.0), F(math.nan), F(math.inf)])
+             heads=[0, 3], kv=0, dim=0, scale=[F(0.0), F(-1.0), F(math.nan), F(math.inf), F(2.5e38)])
     c.refuse(UNSUPPORTED, ldq=1 << 22, ldk=1 << 22, ldv=1 << 22, rows=1 << 31, seqs=1 << 24)
     assert c(dim=129, ldq=2000, ldk=2000, ldv=2000, ldo=2000, **({"lddo": 2000, "lddq": 2000, "lddk": 2000, "lddv": 2000}
                                                                 if "lddo" in c.good else {})) == UNSUPPORTED
@@ -113,10 +113,10 @@ def test_paged_refusals():
              out=A, ldo=32, seqs=2, heads=4, kv=2, dim=8, scale=F(1.0), ws=A, n=1 << 24)
     c.refuse(INVALID, dtype=[3, -1], q=None, kp=None, vp=None, table=None, lengths=None, out=None, ldq=31, ldo=31,
              pages=-1, page=[0, -1], most=[-1, 6], seqs=-1, heads=[0, 3], kv=0, dim=0,
-             scale=[F(0.0), F(-1.0), F(math.nan), F(math.inf)], ws=[None, P(4096 + 128)])
+             scale=[F(0.0), F(-1.0), F(math.nan), F(math.inf), F(2.5e38)], ws=[None, P(4096 + 128)])
     assert c(dim=129, ldq=2000, ldo=2000) == UNSUPPORTED and c(heads=514, ldq=1 << 14, ldo=1 << 14) == UNSUPPORTED
     c.refuse(UNSUPPORTED, page=1 << 31, seqs=1 << 19, pages=1 << 31)
-    assert c(most=1 << 27, ldt=1 << 27) == UNSUPPORTED                        # tokens of a sequence past 2^31
+    assert c(most=(1 << 26) + 1, ldt=1 << 27) == UNSUPPORTED                  # tokens of a sequence past 2^30
     c.refuse(WORKSPACE, n=64)
     assert c(seqs=0, q=None, lengths=None, out=None, table=None) == OK
 
