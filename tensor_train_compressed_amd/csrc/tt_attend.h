@@ -284,8 +284,13 @@ struct Softmax {
     static constexpr float kBias = std::is_same<T, f16>::value ? 8.f : 0.f;
     static constexpr float kSlack = std::is_same<T, f16>::value ? 6.f : 8.f;
     // From here on differences come before products: the rounding of c m, which all
-    // weights share, would be large beside the range of 2^x.
+    // weights share, would be large beside the range of 2^x. Weights are then relative to c m itself,
+    // up to here to c m rounded (mc); where both meet (a reference that moves past the border, a row
+    // beside one past it, parts that are joined), `rest` is what one has and the other has not.
     static constexpr float kFar = 1048576.f;
+    static __device__ __forceinline__ float rest(float m, float mc, float c) {
+        return fabsf(mc) > kFar ? 0.f : fmaf(m, c, -mc);
+    }
     float m, mc, l;   // mc: c m rounded (0 while nothing was seen)
     __device__ __forceinline__ void init() {
         m = -INFINITY;
@@ -314,12 +319,12 @@ struct Softmax {
         }
         float sum = 0.f;
         if (__ballot(fabsf(mc) > kFar)) {
-            const float z = m == -INFINITY ? 0.f : m;
+            const float z = m == -INFINITY ? 0.f : m, add = kBias + rest(z, mc, c);
 #pragma unroll
             for (int b = 0; b < N; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[b][r] = exp2_hw((s[b][r] - z) * c + kBias);
+                    s[b][r] = exp2_hw(fmaf(s[b][r] - z, c, add));
                     sum += s[b][r];
                 }
         } else {
@@ -337,8 +342,9 @@ struct Softmax {
     // What sums relative to maximum m are multiplied by to be relative to `to`.
     static __device__ __forceinline__ float moved(float m, float to, float c) {
         if (m == -INFINITY) return 0.f;
-        const float toc = product(to, c);
-        return fabsf(toc) > kFar ? exp2_hw((m - to) * c) : exp2_hw(product(m, c) - toc);
+        const float mc = product(m, c), toc = product(to, c);
+        if (fabsf(mc) <= kFar && fabsf(toc) <= kFar) return exp2_hw(mc - toc);
+        return exp2_hw((m - to) * c - rest(m, mc, c) + rest(to, toc, c));
     }
     // Both halves' sum; the log of the sum of e^score.
     __device__ __forceinline__ float total() const { return halves_sum(l); }
