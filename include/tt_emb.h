@@ -495,7 +495,9 @@ tt_status tt_emb_rotate_backward(int32_t dtype, int32_t wdtype, const void* q, i
  * gives 0. An infinity or NaN in a row may reach every row of its sequence (a
  * weight of 0 times it), and no other's.
  *   lse  float[heads][rows], log sum_j e^(s_ij), what the backward needs; NULL
- *        when serving
+ *        when serving. Of sums past 256 (TT_F32: 32) from 0 fp32 keeps too few
+ *        digits for weights: the backward forms those rows' maximum and sum
+ *        again, so that no weight is above 1 however large the scores are
  * With 16-bit types the weights e^(s - max) are rounded to dtype before they
  * meet v, and in the backward the weights and dout . v - dout . out times them
  * before they meet the other factors; with TT_F16 the latter must lie in its

@@ -165,7 +165,8 @@ tt_status attend_sizes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv, i
     return TT_OK;
 }
 
-inline size_t delta_bytes(int64_t rows, int64_t heads) {
+// Of one number a row and head: delta, base, ref.
+inline size_t stat_bytes(int64_t rows, int64_t heads) {
     return ((size_t)rows * heads * sizeof(float) + 255) & ~size_t(255);
 }
 
@@ -199,10 +200,10 @@ using namespace tt;
 extern "C" size_t tt_emb_attend_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads,
                                                 int64_t dim) {
     if (attend_sizes(dtype, rows, heads, kv_heads, dim) != TT_OK) return 0;
-    // delta; the splits' sums, at most kGroups workgroups' at these and at fewer rows
+    // delta, base and ref; the splits' sums, at most kGroups workgroups' at these and at fewer rows
     const int64_t most = kGroups * kWaves * kQueries;
     const int64_t sums = std::min(rows * kv_heads * kMaxSplits, most) * 2 * dim;
-    return delta_bytes(rows, heads) + std::max<size_t>(256, ((size_t)sums * sizeof(float) + 255) & ~size_t(255));
+    return 3 * stat_bytes(rows, heads) + std::max<size_t>(256, ((size_t)sums * sizeof(float) + 255) & ~size_t(255));
 }
 
 extern "C" tt_status tt_emb_attend_forward(int32_t dtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
@@ -242,8 +243,9 @@ extern "C" tt_status tt_emb_attend_backward(int32_t dtype, const void* q, int64_
     a.dout = dout; a.lddo = lddo;
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.lddq = lddq; a.lddk = lddk; a.lddv = lddv;
-    a.delta = (float*)workspace;
-    a.part = (float*)((char*)workspace + delta_bytes(rows, heads));
+    a.stats = (float*)workspace;
+    a.apart = (uint32_t)(stat_bytes(rows, heads) / sizeof(float));   // (below 2^28: rows * heads are below 2^27)
+    a.part = (float*)((char*)workspace + 3 * stat_bytes(rows, heads));
     a.splits = (int)splits_of(rows, seqs, kv_heads);
     if (rows == 0 || seqs == 0) return TT_OK;
     const tt_status dq_st = attend_dq(dtype, a);

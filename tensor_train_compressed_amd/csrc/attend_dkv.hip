@@ -22,8 +22,9 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
     typedef Tile<T, DP> L;
     constexpr int BM = tile_rows<T, DP, KEYS>(), BLOCKS = BM / 32, BN = KEYS * kQueries, WAVES = GROUPS * KEYS;
     static_assert(BLOCKS % GROUPS == 0, "a group takes whole blocks");
+    constexpr int STAT = 3 * BM + 4, ROLES = WAVES * 64 >= 3 * BM ? 3 : 2;
     __shared__ __align__(16) char sq0[BM * L::ROW], sd0[BM * L::ROW], sq1[BM * L::ROW], sd1[BM * L::ROW];
-    __shared__ __align__(16) float st0[2 * BM], st1[2 * BM];   // a tile's lse (in powers of two), then its delta
+    __shared__ __align__(16) float st0[STAT], st1[STAT];   // a tile's delta, base and ref, and whether any ref is not 0
     __shared__ __align__(16) char sk[GROUPS == 2 ? BN * L::ROW : 16], sv[GROUPS == 2 ? BN * L::ROW : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = wave / KEYS, mine = wave % KEYS;   // of keys
@@ -42,24 +43,35 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
     TileLoad<T, DP, BM, WAVES, DMA> lq, ld;
     lq.init(a.ldq, a.D, wave);
     ld.init(a.lddo, a.D, wave);
-    float stat = 0.f;   // of query threadIdx.x % BM of the tile
+    // delta, base or ref, by threadIdx.x / BM, of query threadIdx.x % BM of the tile; where there are too few threads for
+    // three, ref apart
+    float stat = 0.f, ref = 0.f;
     auto issue = [&](int i, char* tq, char* td) TT_INLINE {
         const int head = kv * heads + i / per, q0 = (begin + i % per) * BM, left = sp.len - q0;
         const int64_t r = sp.first + q0;
         lq.issue(tq, (const T*)a.q + r * a.ldq + (int64_t)head * a.D, left);
         ld.issue(td, (const T*)a.dout + r * a.lddo + (int64_t)head * a.D, left);
         const int x = threadIdx.x % BM;
-        const bool is_delta = threadIdx.x >= BM;
-        stat = is_delta ? 0.f : INFINITY;
-        if (threadIdx.x < 2 * BM && x < left) {
-            const float f = (is_delta ? a.delta : a.lse)[(int64_t)head * a.rows + r + x];
-            stat = is_delta ? f : log2_sum(f);
+        const int role = threadIdx.x / BM;
+        stat = role == 1 ? INFINITY : 0.f;
+        if (ROLES == 2) ref = 0.f;
+        if (role < ROLES && x < left) {
+            const float* p = a.stats + (int64_t)head * a.rows + r;
+            stat = p[role * a.apart + x];
+            if (ROLES == 2) ref = p[2 * a.apart + x];
         }
     };
     auto store = [&](char* tq, char* td, float* ts) TT_INLINE {
         lq.store(tq);
         ld.store(td);
-        if (threadIdx.x < 2 * BM) ts[threadIdx.x] = stat;
+        if (threadIdx.x < ROLES * BM) ts[threadIdx.x] = stat;
+        if (ROLES == 2 && threadIdx.x < BM) ts[2 * BM + threadIdx.x] = ref;
+        static_assert(ROLES == 3 ? BM % 64 == 0 || BM == 32 : WAVES == 1, "one wave holds a tile's refs");
+        const int holder = ROLES == 3 ? 2 * BM / 64 : 0;
+        if (wave == holder) {
+            const bool any = __ballot(ROLES == 3 ? stat != 0.f && (int)threadIdx.x / BM == 2 : ref != 0.f) != 0;
+            if (lane == 0) reinterpret_cast<int*>(ts)[3 * BM] = any;
+        }
     };
     Piece fk[L::STEPS], fv[L::STEPS];
     if constexpr (GROUPS == 2) {
@@ -84,6 +96,7 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
         landed_barrier();
         if (i + 1 < i1) issue(i + 1, tq, td);
         const int q0 = (begin + i % per) * BM;
+        const bool far = __builtin_amdgcn_readfirstlane(reinterpret_cast<const int*>(st)[3 * BM]) != 0;
         auto scores = [&](int b, floatx16& s, floatx16& dp) TT_INLINE {
             s = dp = floatx16{};
 #pragma unroll
@@ -97,12 +110,21 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
             }
         };
         auto weights = [&](int b, floatx16& s, floatx16& dp) TT_INLINE {
+            if (far) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float m[4];
+                    __builtin_memcpy(m, st + 2 * BM + 32 * b + block_row(4 * g), 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[4 * g + e] -= m[e];
+                }
+            }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float lg[4], dg[4];
                 const int q = 32 * b + block_row(4 * g);
-                __builtin_memcpy(lg, st + q, 16);
-                __builtin_memcpy(dg, st + BM + q, 16);
+                __builtin_memcpy(dg, st + q, 16);
+                __builtin_memcpy(lg, st + BM + q, 16);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = 4 * g + e;

@@ -1,5 +1,5 @@
-// The backward of attention over packed prompts, by queries: dq, and delta for the pass by
-// keys (formulas and layout: attend.hip).
+// The backward of attention over packed prompts, by queries: dq, and what the pass by keys
+// takes of a row, delta and what its weights are relative to (formulas and layout: attend.hip).
 #include "attend.h"
 
 namespace tt {
@@ -11,6 +11,9 @@ namespace {
 // dk (2-norm errors 0.0026 instead of 0.0017 for rounding the results alone). Tiles of up to this many keys
 // are gone over once more for the second.
 constexpr int kExact = 256;
+
+// What a sweep over the keys forms: maximum and sum of a row's weights, delta, dq.
+enum Sweep { STATS, DELTA, GRADIENT };
 
 template <class T, int DP, bool DMA, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_attend_dq(const AttendArgs a) {
@@ -59,35 +62,54 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
         }
         delta = halves_sum(delta);
     }
-    float lse2 = INFINITY;
-    if (there) lse2 = log2_sum(a.lse[(int64_t)job.head * a.rows + row]);
+    // weights are 2^(c (s - ref) - base); ref is 0 where lse is taken as it is
+    float lse = 0.f, base = INFINITY, ref = 0.f;
+    if (there) {
+        lse = a.lse[(int64_t)job.head * a.rows + row];
+        base = log2_sum(lse);
+    }
     const float c = a.scale * kLog2e;
     floatx16 dq[DP / 32] = {};
     float sum = 0.f;   // of p (dout . v)
+    bool far = false;  // any of the wave's rows has a ref
+    Softmax<T> sm;
     store_first();
-    // DELTA: forms that sum alone
-    auto step = [&](auto only_delta, int k0, const char* sk, const char* sv, char* tk, char* tv) TT_INLINE {
-        constexpr bool DELTA = only_delta;
+    auto step = [&](auto sweep, int k0, const char* sk, const char* sv, char* tk, char* tv) TT_INLINE {
+        constexpr Sweep SWEEP = sweep;
         landed_barrier();
         const int next = k0 + BN;
         if (next < last) {
             lk.issue(tk, pk + next * a.ldk, sp.len - next);
-            lv.issue(tv, pv + next * a.ldv, sp.len - next);
+            if constexpr (SWEEP != STATS) lv.issue(tv, pv + next * a.ldv, sp.len - next);
         }
         if (k0 < mine) {
 #pragma unroll
             for (int b = 0; b < BLOCKS; ++b) {
-                floatx16 s = {}, dp = {};
-                auto weights = [&]() TT_INLINE {
+                if constexpr (SWEEP == STATS) {
+                    floatx16 s[1] = {};
+#pragma unroll
+                    for (int x = 0; x < L::STEPS; ++x) s[0] = mma_rows<T>(L::row_piece(sk, 32 * b, x), fq[x], s[0]);
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        s[r] = exp2_hw(fmaf(s[r], c, -lse2)) * (DELTA ? dp[r] : dp[r] - delta);
+                        if (k0 + 32 * b + block_row(r) >= limit) s[0][r] = -INFINITY;
+                    sm.step(s, c, [](float) {});
+                    continue;
+                }
+                floatx16 s = {}, dp = {};
+                auto weights = [&]() TT_INLINE {
+                    if (far) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[r] -= ref;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[r] = exp2_hw(fmaf(s[r], c, -base)) * (SWEEP == DELTA ? dp[r] : dp[r] - delta);
                     if (k0 + 32 * (b + 1) > whole) {
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
                             if (k0 + 32 * b + block_row(r) >= limit) s[r] = 0.f;
                     }
-                    if constexpr (DELTA)
+                    if constexpr (SWEEP == DELTA)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) sum += s[r];
                 };
@@ -98,7 +120,7 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
                     auto fetch = [&](auto slot) TT_INLINE {
                         constexpr int u = slot, t = u - N;
                         if constexpr (u < N) f[u % AHEAD] = L::row_piece(u % 2 ? sv : sk, 32 * b, u / 2);
-                        else if constexpr (!DELTA && t < 2 * J) f[u % AHEAD] = L::column_piece(sk, 32 * b + 16 * (t / J), t % J);
+                        else if constexpr (SWEEP == GRADIENT && t < 2 * J) f[u % AHEAD] = L::column_piece(sk, 32 * b + 16 * (t / J), t % J);
                     };
                     each<AHEAD>(fetch);
                     each<N>([&](auto slot) TT_INLINE {
@@ -110,7 +132,7 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
                     });
                     __builtin_amdgcn_sched_barrier(0);
                     weights();
-                    if constexpr (DELTA) continue;
+                    if constexpr (SWEEP == DELTA) continue;
                     w.set(s);
                     each<2 * J>([&](auto slot) TT_INLINE {
                         constexpr int t = slot, j = t % J;
@@ -134,26 +156,55 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
         }
         if (next < last) {
             lk.store(tk);
-            lv.store(tv);
+            if constexpr (SWEEP != STATS) lv.store(tv);
         }
     };
-    auto sweep = [&](auto only_delta) TT_INLINE {
+    auto over = [&](auto sweep) TT_INLINE {
         for (int k0 = 0; k0 < last; k0 += 2 * BN) {
-            step(only_delta, k0, sk0, sv0, sk1, sv1);
-            if (k0 + BN < last) step(only_delta, k0 + BN, sk1, sv1, sk0, sv0);
+            step(sweep, k0, sk0, sv0, sk1, sv1);
+            if (k0 + BN < last) step(sweep, k0 + BN, sk1, sv1, sk0, sv0);
         }
     };
+    auto again = [&]() TT_INLINE {
+        __syncthreads();
+        issue_first();
+        store_first();
+    };
+    const bool past = !(fabsf(lse) <= trusted_lse<T>());
+    int any = __ballot(past) != 0;
+    if constexpr (WAVES > 1) {   // (the waves', in a tile's place that nothing was sent for yet)
+        int* flags = reinterpret_cast<int*>(sk1);
+        if (lane == 0) flags[wave] = any;
+        landed_barrier();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) any |= flags[w];
+        any = __builtin_amdgcn_readfirstlane(any);
+    }
+    if (any) {
+        sm.init();
+        over(std::integral_constant<Sweep, STATS>{});
+        const float total = sm.total();
+        if (past) {
+            ref = sm.m == -INFINITY ? 0.f : sm.m;
+            base = total == 0.f ? INFINITY : log2f(total) - Softmax<T>::kBias - Softmax<T>::rest(ref, sm.mc, c);
+        }
+        far = __ballot(ref != 0.f) != 0;
+        again();
+    }
     if constexpr (sizeof(T) == 2) {
         if (last <= kExact) {
-            sweep(std::true_type{});
+            over(std::integral_constant<Sweep, DELTA>{});
             delta = halves_sum(sum);
-            __syncthreads();
-            issue_first();
-            store_first();
+            again();
         }
     }
-    if (there && lane < 32) a.delta[(int64_t)job.head * a.rows + row] = delta;
-    sweep(std::false_type{});
+    if (there && lane < 32) {
+        float* p = a.stats + (int64_t)job.head * a.rows + row;
+        p[0] = delta;
+        p[a.apart] = base;
+        p[2 * a.apart] = ref;
+    }
+    over(std::integral_constant<Sweep, GRADIENT>{});
     if (there) store_columns<T, DP>((T*)a.dq + row * a.lddq + at, dq, a.scale, a.D);
 }
 

@@ -112,3 +112,149 @@ def test_paged_parts_on_both_sides_of_the_border(length):
         want = p @ vi
         bound = (e + 2 * product_slack(length) * p) @ vi.abs() + want.abs() * e.sum() + rounded(F32, want)
         check(out, want, bound, f"paged border {m} {length}")
+
+
+# --------------------------------------------------- gradients at large scores
+
+# |lse| up to which the backward takes it as it is (past that it forms maximum and sum again): four roundings of it and the
+# conversions' constants, 5 U32 |lse|, are then what a weight is off by
+TRUSTED = {F32: 32.0, BF16: 256.0, F16: 256.0}
+
+
+def parts_of(t, heads):
+    """[rows, heads * dim] as [heads, rows, dim] in 64 bits."""
+    return t.double().reshape(t.shape[0], heads, -1).transpose(0, 1)
+
+
+def exact_backward(q, k, v, dout, heads, kv, causal, scale):
+    """dq, dk, dv of one sequence whose scores q . k are exact in fp32, and their bounds (those of tests/attend_ref.py, with
+    a weight's error that does not grow with the scores)."""
+    t, n = q.dtype, q.shape[0]
+    g = heads // kv
+    u = U[t] if t != F32 else 0.0
+    q, dout = parts_of(q, heads), parts_of(dout, heads)
+    k, v = (parts_of(x, kv).repeat_interleave(g, 0) for x in (k, v))
+    kd, kn, kq = product_slack(q.shape[2]), product_slack(n), product_slack(g * n)
+    seen = torch.ones(n, n, dtype=torch.bool, device=q.device)
+    if causal:
+        seen = seen.tril()
+    s = (scale * q @ k.mT).masked_fill(~seen, -torch.inf)
+    lse = torch.logsumexp(s, -1, keepdim=True)
+    p = torch.softmax(s, -1)
+    x = (lse - s).clamp(0, 128)
+    e = 8 * U32 * (1 + x) + 5 * U32 * lse.abs().clamp(max=TRUSTED[t]) + kn
+    out = p @ v
+    # the forward's: its weights rounded too
+    bo = rounded(t, out) + (p * (e + u + kn)) @ v.abs() + out.abs() * (p * e).sum(-1, keepdim=True)
+    dp = dout @ v.mT
+    delta = (dout * out).sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    ddelta = (dout.abs() * bo).sum(-1, keepdim=True) + kd * (dout * out).abs().sum(-1, keepdim=True)
+    eds = p * (e * (dp - delta).abs() + kd * (dout.abs() @ v.abs().mT) + ddelta + 4 * U32 * (dp.abs() + delta.abs()))
+    # weights below 2^-126 are 0: an error of that size, times what the weight is multiplied by
+    eds = eds + u * (ds.abs() + eds) + 2.0 ** -126 * (dp.abs() + delta.abs()) * seen
+    ep = p * (e + u)
+    # f16: a product's rounding below its normal numbers (2^-25 of it), the factors' largest being 2^9 or more, of a row's
+    # for dq and of a column's for dk; weights are at 2^14
+    low = (lambda d: 2.0 ** -34 * ds.abs().amax(d, keepdim=True) * seen) if t == F16 else (lambda d: 2.0 ** -126 * seen)
+    group = lambda y: y.view(kv, g, n, -1).sum(1)   # noqa: E731
+    dq, dk, dv = scale * ds @ k, scale * group(ds.mT @ q), group(p.mT @ dout)
+    bq = rounded(t, dq) + scale * (eds + low(-1) + kn * ds.abs()) @ k.abs()
+    bk = rounded(t, dk) + scale * group((eds + low(-2) + kq * ds.abs()).mT @ q.abs())
+    bv = rounded(t, dv) + group((ep + (2.0 ** -39 if t == F16 else 2.0 ** -126) * seen + kq * p).mT @ dout.abs())
+    flat = lambda y: y.transpose(0, 1).flatten(1)   # noqa: E731
+    return [flat(y) for y in (dq, dk, dv)], [flat(y) for y in (bq, bk, bv)]
+
+
+def check_backward(q, k, v, dout, lengths, heads, kv, causal, scale, what):
+    say("attend's range", what, q.dtype, lengths, heads, kv, q.shape[1] // heads, causal, scale)
+    off = offsets_of(lengths)
+    out, lse = torch.empty_like(dout), torch.empty(heads, q.shape[0], device=DEV)
+    how = dict(heads=heads, kv_heads=kv, causal=causal, scale=scale)
+    tte.tt_emb_attend_forward(q, k, v, off, out, lse, **how)
+    got = [torch.empty(t.shape, dtype=t.dtype, device=DEV) for t in (q, k, v)]
+    tte.tt_emb_attend_backward(q, k, v, off, out, lse, dout, *got, **how)
+    at = 0
+    for n in lengths:
+        r, at = slice(at, at + n), at + n
+        want, bound = exact_backward(q[r], k[r], v[r], dout[r], heads, kv, causal, scale)
+        for a, w, b, name in zip(got, want, bound, ("dq", "dk", "dv")):
+            check(a[r], w, b, f"{what}: {name}")
+
+
+WIDE = pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+SHAPES = pytest.mark.parametrize("lengths,heads,kv,dim,pad", [
+    ([300], 2, 1, 64, 0), ([100, 60], 4, 2, 128, 0), ([300], 2, 2, 128, 0), ([290], 2, 1, 33, 1), ([300, 5], 2, 1, 128, 3),
+    ([20, 24, 1, 31], 4, 4, 32, 0), ([200], 64, 32, 96, 0), ([330, 182], 64, 64, 64, 0)])
+
+
+def spaced(t, pad):
+    wide = torch.zeros(t.shape[0], t.shape[1] + pad, dtype=t.dtype, device=DEV)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+@WIDE
+@SHAPES
+@pytest.mark.parametrize("scale", [2.0 ** -7, 2.0 ** -3, 4.0])
+def test_gradients_of_sharp_scores(dt, lengths, heads, kv, dim, pad, scale):
+    """Queries and keys of whole numbers: scores of up to some 10^4 that fp32 holds."""
+    rows = sum(lengths)
+    q, k = (spaced((rand(rows, n * dim, seed=s) * 12).round().clamp(-40, 40).to(dt), pad) for n, s in ((heads, 1), (kv, 2)))
+    v = spaced(rand(rows, kv * dim, seed=3, dt=dt), pad)
+    dout = spaced((rand(rows, heads * dim, seed=4) * (2.0 ** -8 if dt == F16 else 1.0)).to(dt), pad)
+    for causal in (True, False):
+        check_backward(q, k, v, dout, lengths, heads, kv, causal, scale, "sharp")
+
+
+@WIDE
+@SHAPES
+@pytest.mark.parametrize("size", [2.0 ** 4, 2.0 ** 10, 2.0 ** 13, 2.0 ** 17, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100])
+def test_gradients_of_huge_scores(dt, lengths, heads, kv, dim, pad, size):
+    """The keys with a row's largest score share its weight, however large that is; by the operands and by the scale."""
+    if dt == F16 and size > 2.0 ** 13:
+        pytest.skip("gradients past f16's range")
+    rows = sum(lengths)
+    j = torch.arange(rows, device=DEV)
+    for by_scale in (True, False):
+        a, b = (1.0, size) if by_scale else (size, 1.0)
+        q, k = torch.zeros(rows, heads, dim, device=DEV), torch.zeros(rows, kv, dim, device=DEV)
+        q[:, :, dim // 2] = torch.where(j % 2 == 0, a, -a)[:, None]
+        k[:, :, dim // 2] = (j % 50 - 25)[:, None].float()
+        q, k = (spaced(t.flatten(1).to(dt), pad) for t in (q, k))
+        v = spaced(rand(rows, kv * dim, seed=3, dt=dt), pad)
+        dout = spaced((rand(rows, heads * dim, seed=4) * (2.0 ** -8 if dt == F16 else 1.0)).to(dt), pad)
+        check_backward(q, k, v, dout, lengths, heads, kv, False, b, f"huge {size} {'scale' if by_scale else 'query'}")
+
+
+@WIDE
+def test_gradients_do_not_depend_on_the_rows_beside(dt):
+    """Rows past what the kept sum holds do not change the gradients of the queries beside them whose sum is taken as it
+    is, to the bit (given the same outputs and sums of theirs)."""
+    n, dim = 200, 64
+    q, k, v, d = ((rand(n, dim, seed=s) * 4).round().to(dt) for s in range(1, 5))
+    off = offsets_of([n])
+    own = torch.arange(n, device=DEV) % 3 != 0
+    res, kept = [], None
+    for far in (False, True):
+        x = q.clone()
+        if far:
+            x[::3] *= 16.0
+        out, lse = torch.empty_like(q), torch.empty(1, n, device=DEV)
+        how = dict(heads=1, kv_heads=1, causal=True, scale=0.125)
+        tte.tt_emb_attend_forward(x, k, v, off, out, lse, **how)
+        kept = kept or (out.clone(), lse.clone())
+        out[own], lse[:, own] = kept[0][own], kept[1][:, own]
+        g = [torch.empty_like(q) for _ in range(3)]
+        tte.tt_emb_attend_backward(x, k, v, off, out, lse, d, *g, **how)
+        assert bool((lse[0].abs() > TRUSTED[dt]).any()) or not far
+        res.append(g[0])
+    own &= kept[1][0].abs() <= TRUSTED[dt]
+    assert int(own.sum()) > 20 and torch.equal(res[0][own], res[1][own])
+
+
+@WIDE
+def test_sharp_attention_trained(dt):
+    """The sharp scale of the forward's test, with its gradients."""
+    from tests.test_attend_gpu import check_attend
+    check_attend(dt, [150, 90], 2, 1, 64, scale=30.0)
