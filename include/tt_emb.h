@@ -500,8 +500,9 @@ tt_status tt_emb_rotate_backward(int32_t dtype, int32_t wdtype, const void* q, i
  *        again, so that no weight is above 1 however large the scores are
  * With 16-bit types the weights e^(s - max) are rounded to dtype before they
  * meet v, and in the backward the weights and dout . v - dout . out times them
- * before they meet the other factors; with TT_F16 the latter must lie in its
- * range. Offsets that decrease or lie outside the rows leave the outputs
+ * before they meet the other factors. With TT_F16 both go there times powers
+ * of two that hold the largest within its range and those down to 2^-23 of it
+ * at its full digits, whatever the size of dout. Offsets that decrease or lie outside the rows leave the outputs
  * unspecified. The workspace is the backward's.
  * Limits: 0 < scale < 2e38; dim <= 128, rows < 2^31, row strides < 2^22,
  * (rows / 32 + seqs) * heads <= 2^22. */

@@ -66,6 +66,45 @@ constexpr int waves_of() {
     return DP <= 64 || DMA ? 2 : 1;
 }
 
+// A sum's f16 factors (the backward's ds), times a power of two 2^up that keeps the largest of a column that was
+// seen between 2^9 and 2^15: none is past f16's range, and those down to 2^-23 of the largest keep their digits.
+// The power falls where a factor outgrows it, and sums are multiplied by what it fell. Other types hold any factor.
+// Its cost, dq, dk and dv together: 8192 rows, 32 and 8 heads of 128, 1900 -> 2000 us; 16 and 2 heads of 64 in 8
+// sequences 185 -> 200.
+template <class T>
+struct Range {
+    static constexpr bool kOn = std::is_same<T, f16>::value;
+    static constexpr float kMost = 32768.f;
+    float up;
+    __device__ __forceinline__ void init() { up = kOn ? 60.f : 0.f; }   // (f16's products, of at most 2^53, stay finite)
+    // Takes factors that are multiplied by 2^up already.
+    template <class F>
+    __device__ __forceinline__ void step(floatx16& x, F rescale) {
+        if constexpr (kOn) {
+            float top = 0.f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
+            top = halves_max(top);
+            if (__ballot(top > kMost)) {
+                // top is below 2^e: to below 2^10 (infinite: it stays)
+                const int e = top > kMost && top < INFINITY ? 10 - __builtin_amdgcn_frexp_expf(top) : 0;
+                const float a = ldexpf(1.f, e);
+                up += (float)e;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] *= a;
+                rescale(a);
+            }
+        }
+    }
+    // What sums are multiplied by at the end.
+    __device__ __forceinline__ float back() const { return ldexpf(1.f, -(int)up); }
+};
+// Weights on their way to f16, which are 1 at most, in powers of two: those down to 2^-28 keep their digits.
+template <class T>
+constexpr float weight_bits() {
+    return Range<T>::kOn ? 14.f : 0.f;
+}
+
 // The workgroup's tile and head: heads that share keys lie next to each other.
 struct Job {
     int64_t tile;

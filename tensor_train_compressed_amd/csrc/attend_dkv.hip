@@ -51,25 +51,25 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
         const int64_t r = sp.first + q0;
         lq.issue(tq, (const T*)a.q + r * a.ldq + (int64_t)head * a.D, left);
         ld.issue(td, (const T*)a.dout + r * a.lddo + (int64_t)head * a.D, left);
-        const int x = threadIdx.x % BM;
-        const int role = threadIdx.x / BM;
+        // (tiles of 64 rows: a wave has one role)
+        const int x = BM == 64 ? lane : threadIdx.x % BM, role = BM == 64 ? wave : threadIdx.x / BM;
         stat = role == 1 ? INFINITY : 0.f;
         if (ROLES == 2) ref = 0.f;
         if (role < ROLES && x < left) {
             const float* p = a.stats + (int64_t)head * a.rows + r;
-            stat = p[role * a.apart + x];
+            stat = (p + role * a.apart)[x] - (role == 1 ? weight_bits<T>() : 0.f);
             if (ROLES == 2) ref = p[2 * a.apart + x];
         }
     };
     auto store = [&](char* tq, char* td, float* ts) TT_INLINE {
         lq.store(tq);
         ld.store(td);
-        if (threadIdx.x < ROLES * BM) ts[threadIdx.x] = stat;
+        if (BM == 64 ? wave < ROLES : threadIdx.x < ROLES * BM) ts[threadIdx.x] = stat;
         if (ROLES == 2 && threadIdx.x < BM) ts[2 * BM + threadIdx.x] = ref;
         static_assert(ROLES == 3 ? BM % 64 == 0 || BM == 32 : WAVES == 1, "one wave holds a tile's refs");
         const int holder = ROLES == 3 ? 2 * BM / 64 : 0;
         if (wave == holder) {
-            const bool any = __ballot(ROLES == 3 ? stat != 0.f && (int)threadIdx.x / BM == 2 : ref != 0.f) != 0;
+            const bool any = __ballot(ROLES == 3 ? stat != 0.f && (BM == 64 || threadIdx.x / BM == 2) : ref != 0.f) != 0;
             if (lane == 0) reinterpret_cast<int*>(ts)[3 * BM] = any;
         }
     };
@@ -91,6 +91,8 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
     if (GROUPS == 2 && group == 0) __builtin_amdgcn_s_setprio(1);
     const float c = a.scale * kLog2e;
     floatx16 dk[DP / 32] = {}, dv[DP / 32] = {};
+    Range<T> range;   // of the keys
+    range.init();
     store(sq0, sd0, st0);
     auto step = [&](int i, const char* sq, const char* sd, const float* st, char* tq, char* td, float* ts) TT_INLINE {
         landed_barrier();
@@ -181,6 +183,15 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
                     }
                 }
                 ws.set(s);
+                if constexpr (Range<T>::kOn) {
+                    const float f = exp2_hw(range.up);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) dp[r] *= f;
+                }
+                range.step(dp, [&](float f) TT_INLINE {
+#pragma unroll
+                    for (int j = 0; j < DP / 32; ++j) dk[j] *= f;
+                });
                 wd.set(dp);
                 each<4 * (DP / 32)>([&](auto slot) TT_INLINE {
                     constexpr int t = slot, j = t / 2 % (DP / 32), h = t / 2 / (DP / 32);
@@ -218,6 +229,14 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
     for (int i = i0; i < i1; i += 2) {
         step(i, sq0, sd0, st0, sq1, sd1, st1);
         if (i + 1 < i1) step(i + 1, sq1, sd1, st1, sq0, sd0, st0);
+    }
+    if constexpr (Range<T>::kOn) {
+        const float wb = exp2f(-weight_bits<T>());
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) {
+            dk[j] = dk[j] * range.back() * wb;
+            dv[j] *= wb;
+        }
     }
     if constexpr (GROUPS == 2) {
         landed_barrier();   // (keys and values of a split without queries may be under way)

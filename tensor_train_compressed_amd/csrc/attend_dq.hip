@@ -73,6 +73,8 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
     float sum = 0.f;   // of p (dout . v)
     bool far = false;  // any of the wave's rows has a ref
     Softmax<T> sm;
+    Range<T> range;
+    range.init();
     store_first();
     auto step = [&](auto sweep, int k0, const char* sk, const char* sv, char* tk, char* tv) TT_INLINE {
         constexpr Sweep SWEEP = sweep;
@@ -101,9 +103,10 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
 #pragma unroll
                         for (int r = 0; r < 16; ++r) s[r] -= ref;
                     }
+                    const float z = SWEEP == GRADIENT ? range.up - base : -base;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        s[r] = exp2_hw(fmaf(s[r], c, -base)) * (SWEEP == DELTA ? dp[r] : dp[r] - delta);
+                        s[r] = exp2_hw(fmaf(s[r], c, z)) * (SWEEP == DELTA ? dp[r] : dp[r] - delta);
                     if (k0 + 32 * (b + 1) > whole) {
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
@@ -133,6 +136,10 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
                     __builtin_amdgcn_sched_barrier(0);
                     weights();
                     if constexpr (SWEEP == DELTA) continue;
+                    range.step(s, [&](float f) TT_INLINE {
+#pragma unroll
+                        for (int j = 0; j < J; ++j) dq[j] *= f;
+                    });
                     w.set(s);
                     each<2 * J>([&](auto slot) TT_INLINE {
                         constexpr int t = slot, j = t % J;
@@ -205,6 +212,10 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
         p[2 * a.apart] = ref;
     }
     over(std::integral_constant<Sweep, GRADIENT>{});
+    if constexpr (Range<T>::kOn) {
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) dq[j] *= range.back();
+    }
     if (there) store_columns<T, DP>((T*)a.dq + row * a.lddq + at, dq, a.scale, a.D);
 }
 

@@ -126,9 +126,9 @@ def parts_of(t, heads):
     return t.double().reshape(t.shape[0], heads, -1).transpose(0, 1)
 
 
-def exact_backward(q, k, v, dout, heads, kv, causal, scale):
-    """dq, dk, dv of one sequence whose scores q . k are exact in fp32, and their bounds (those of tests/attend_ref.py, with
-    a weight's error that does not grow with the scores)."""
+def exact_backward(q, k, v, dout, heads, kv, causal, scale, score_sums=False):
+    """dq, dk, dv of one sequence whose scores q . k are exact in fp32 (or, with score_sums, are off by what their sums round),
+    and their bounds: those of tests/attend_ref.py, with a weight's error that does not grow with the scores."""
     t, n = q.dtype, q.shape[0]
     g = heads // kv
     u = U[t] if t != F32 else 0.0
@@ -143,6 +143,8 @@ def exact_backward(q, k, v, dout, heads, kv, causal, scale):
     p = torch.softmax(s, -1)
     x = (lse - s).clamp(0, 128)
     e = 8 * U32 * (1 + x) + 5 * U32 * lse.abs().clamp(max=TRUSTED[t]) + kn
+    if score_sums:
+        e = e + kd * scale * (q.abs() @ k.abs().mT)
     out = p @ v
     # the forward's: its weights rounded too
     bo = rounded(t, out) + (p * (e + u + kn)) @ v.abs() + out.abs() * (p * e).sum(-1, keepdim=True)
@@ -154,13 +156,18 @@ def exact_backward(q, k, v, dout, heads, kv, causal, scale):
     # weights below 2^-126 are 0: an error of that size, times what the weight is multiplied by
     eds = eds + u * (ds.abs() + eds) + 2.0 ** -126 * (dp.abs() + delta.abs()) * seen
     ep = p * (e + u)
-    # f16: a product's rounding below its normal numbers (2^-25 of it), the factors' largest being 2^9 or more, of a row's
-    # for dq and of a column's for dk; weights are at 2^14
-    low = (lambda d: 2.0 ** -34 * ds.abs().amax(d, keepdim=True) * seen) if t == F16 else (lambda d: 2.0 ** -126 * seen)
+    # f16: half a step below its normal numbers is 2^-25; the largest factor of a row (dq) and of a key over the heads that
+    # share it (dk) is multiplied to 2^9 or more, none by more than 2^60; weights by 2^14
+    def low(by_key):
+        if t != F16:
+            return 2.0 ** -126 * seen
+        top = ds.abs().amax(-2, keepdim=True).view(kv, g, 1, n).amax(1).repeat_interleave(g, 0) if by_key else \
+            ds.abs().amax(-1, keepdim=True)
+        return (2.0 ** -34 * top + 2.0 ** -85) * seen
     group = lambda y: y.view(kv, g, n, -1).sum(1)   # noqa: E731
     dq, dk, dv = scale * ds @ k, scale * group(ds.mT @ q), group(p.mT @ dout)
-    bq = rounded(t, dq) + scale * (eds + low(-1) + kn * ds.abs()) @ k.abs()
-    bk = rounded(t, dk) + scale * group((eds + low(-2) + kq * ds.abs()).mT @ q.abs())
+    bq = rounded(t, dq) + scale * (eds + low(False) + kn * ds.abs()) @ k.abs()
+    bk = rounded(t, dk) + scale * group((eds + low(True) + kq * ds.abs()).mT @ q.abs())
     bv = rounded(t, dv) + group((ep + (2.0 ** -39 if t == F16 else 2.0 ** -126) * seen + kq * p).mT @ dout.abs())
     flat = lambda y: y.transpose(0, 1).flatten(1)   # noqa: E731
     return [flat(y) for y in (dq, dk, dv)], [flat(y) for y in (bq, bk, bv)]
@@ -182,7 +189,6 @@ def check_backward(q, k, v, dout, lengths, heads, kv, causal, scale, what):
             check(a[r], w, b, f"{what}: {name}")
 
 
-WIDE = pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 SHAPES = pytest.mark.parametrize("lengths,heads,kv,dim,pad", [
     ([300], 2, 1, 64, 0), ([100, 60], 4, 2, 128, 0), ([300], 2, 2, 128, 0), ([290], 2, 1, 33, 1), ([300, 5], 2, 1, 128, 3),
     ([20, 24, 1, 31], 4, 4, 32, 0), ([200], 64, 32, 96, 0), ([330, 182], 64, 64, 64, 0)])
@@ -194,7 +200,7 @@ def spaced(t, pad):
     return wide[:, :t.shape[1]]
 
 
-@WIDE
+@TYPES
 @SHAPES
 @pytest.mark.parametrize("scale", [2.0 ** -7, 2.0 ** -3, 4.0])
 def test_gradients_of_sharp_scores(dt, lengths, heads, kv, dim, pad, scale):
@@ -207,7 +213,7 @@ def test_gradients_of_sharp_scores(dt, lengths, heads, kv, dim, pad, scale):
         check_backward(q, k, v, dout, lengths, heads, kv, causal, scale, "sharp")
 
 
-@WIDE
+@TYPES
 @SHAPES
 @pytest.mark.parametrize("size", [2.0 ** 4, 2.0 ** 10, 2.0 ** 13, 2.0 ** 17, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100])
 def test_gradients_of_huge_scores(dt, lengths, heads, kv, dim, pad, size):
@@ -227,7 +233,7 @@ def test_gradients_of_huge_scores(dt, lengths, heads, kv, dim, pad, size):
         check_backward(q, k, v, dout, lengths, heads, kv, False, b, f"huge {size} {'scale' if by_scale else 'query'}")
 
 
-@WIDE
+@TYPES
 def test_gradients_do_not_depend_on_the_rows_beside(dt):
     """Rows past what the kept sum holds do not change the gradients of the queries beside them whose sum is taken as it
     is, to the bit (given the same outputs and sums of theirs)."""
@@ -253,8 +259,55 @@ def test_gradients_do_not_depend_on_the_rows_beside(dt):
     assert int(own.sum()) > 20 and torch.equal(res[0][own], res[1][own])
 
 
-@WIDE
+@TYPES
 def test_sharp_attention_trained(dt):
     """The sharp scale of the forward's test, with its gradients."""
     from tests.test_attend_gpu import check_attend
     check_attend(dt, [150, 90], 2, 1, 64, scale=30.0)
+
+
+# ----------------------------------------------------- f16: the size of gradients
+
+@pytest.mark.parametrize("lengths,heads,kv,dim,pad", [
+    ([2048], 2, 1, 64, 0), ([1500], 2, 2, 128, 0), ([1111], 2, 1, 33, 1), ([900], 1, 1, 128, 3), ([120, 100, 128], 4, 2, 32, 0),
+    ([700], 64, 32, 64, 0)])
+@pytest.mark.parametrize("size", [2.0 ** -6, 2.0 ** -10, 2.0 ** -13])
+@pytest.mark.parametrize("large", ["q", "k"])
+def test_small_f16_gradients(lengths, heads, kv, dim, pad, size, large):
+    """Gradients of the outputs far below 1, whose products with weights are below f16's range: those of queries, keys and
+    values keep their digits. Large keys or queries bring the results back into it."""
+    rows = sum(lengths)
+    sq, sk = (2.0 ** 5, 2.0 ** -5) if large == "q" else (2.0 ** -5, 2.0 ** 5)
+    q, k, v, dout = (spaced((rand(rows, n * dim, seed=s) * m).to(F16), pad) for n, s, m in (
+        (heads, 1, sq), (kv, 2, sk), (kv, 3, 0.25), (heads, 4, size)))
+    # scores of unit normals, not exact: 64 bits' of the same operands, within their sums' roundings
+    check_small(q, k, v, dout, lengths, heads, kv, dim ** -0.5, "small")
+
+
+@pytest.mark.parametrize("lengths,heads,kv,dim,pad", [([8, 31], 4, 2, 64, 0), ([300], 2, 1, 128, 0), ([40], 2, 1, 33, 1)])
+def test_large_f16_gradients(lengths, heads, kv, dim, pad):
+    """Products of the outputs' gradients with the values past f16's range, where the results are within it."""
+    rows = sum(lengths)
+    q, k, v, dout = (spaced((rand(rows, n * dim, seed=s) * m).to(F16), pad) for n, s, m in (
+        (heads, 1, 2.0 ** -7), (kv, 2, 2.0 ** -7), (kv, 3, 2.0 ** 5), (heads, 4, 2.0 ** 10)))
+    dp = parts_of(dout, heads)[0, :8] @ parts_of(v, kv)[0, :8].mT
+    assert float(dp.abs().max()) > 2 * 65504
+    check_small(q, k, v, dout, lengths, heads, kv, dim ** -0.5, "large")
+
+
+def check_small(q, k, v, dout, lengths, heads, kv, scale, what):
+    """check_backward with the roundings of scores that are not exact, in fp32 sums: what they take to weights and through
+    them to the results, beside its bounds."""
+    off = offsets_of(lengths)
+    say("attend's f16 gradients", what, lengths, heads, kv, q.shape[1] // heads, float(dout.abs().max()))
+    out, lse = torch.empty_like(dout), torch.empty(heads, q.shape[0], device=DEV)
+    how = dict(heads=heads, kv_heads=kv, causal=False, scale=scale)
+    tte.tt_emb_attend_forward(q, k, v, off, out, lse, **how)
+    got = [torch.empty(t.shape, dtype=t.dtype, device=DEV) for t in (q, k, v)]
+    tte.tt_emb_attend_backward(q, k, v, off, out, lse, dout, *got, **how)
+    at = 0
+    for n in lengths:
+        r, at = slice(at, at + n), at + n
+        want, bound = exact_backward(q[r], k[r], v[r], dout[r], heads, kv, False, scale, score_sums=True)
+        for a, w, b, name in zip(got, want, bound, ("dq", "dk", "dv")):
+            check(a[r], w, b, f"{what}: {name}")
