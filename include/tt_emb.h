@@ -524,7 +524,8 @@ tt_status tt_emb_attend_backward(int32_t dtype, const void* q, int64_t ldq, cons
  * j < lengths[s] (int64; the new token's own key and value are in the cache
  * already). A length past most_pages * page_size counts as that, one below zero
  * as zero; a token whose page is outside [0, pages) is not seen; a sequence
- * that sees nothing gives 0.
+ * that sees nothing gives 0. With 16-bit types weights meet v in two parts of
+ * dtype, so that their rounding does not show beside the output's.
  *   table  int32, most_pages entries a sequence, ldt apart
  * The workspace serves any lengths, and fewer sequences.
  * Limits: 0 < scale < 2e38; dim <= 128, heads / kv_heads <= 256,

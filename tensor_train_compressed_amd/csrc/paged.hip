@@ -6,7 +6,7 @@
 // key head (a wave's 32 columns are these heads). A sequence's tokens are split over
 // workgroups and, there, over waves, each with a softmax of its own; waves are joined in
 // LDS and workgroups, where a sequence has several, by a second launch, in a fixed order.
-// 64 sequences of 8000 tokens, 8 key heads of 128 bf16: 1.8 GB in 371 us, 4.9 TB/s; one of 32768:
+// 64 sequences of 8000 tokens, 8 key heads of 128 bf16: 1.8 GB in 373 us, 4.8 TB/s; one of 32768:
 // 134 MB in 25 us and 4.6 to join.
 #include "tt_attend.h"
 
@@ -171,8 +171,23 @@ __global__ __launch_bounds__(kWaves * 64, (DMA && sizeof(T) == 2) || DP == 32 ? 
         });
         Weights<T> w;
         w.set(s[0]);
+        if constexpr (sizeof(T) == 2) {
+            // the second part (see Weights)
+            Weights<T> low;
+            s[0] = w.rest(s[0]);
+            low.set(s[0]);
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j) o[j] = mma_columns<T, DP>(sv, 0, j, w, o[j]);
+            for (int j = 0; j < DP / 32; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const Piece x = L::column_piece(sv, 16 * t, j);
+                    o[j] = mma16<T>(x, w.w[t], o[j]);
+                    o[j] = mma16<T>(x, low.w[t], o[j]);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < DP / 32; ++j) o[j] = mma_columns<T, DP>(sv, 0, j, w, o[j]);
+        }
         if (DMA && next < end) {
             taken();
             send(a.v, sv, rv);

@@ -144,7 +144,12 @@ struct Tile {
     }
 };
 
-// A 32 x 32 product's result as the second operand of one by columns.
+// A 32 x 32 product's result as the second operand of one by columns. 16-bit types: rounded
+// to T, once or in two parts, the second what the first rounds off. Outputs' 2-norm errors of bf16 (f16) are
+// 0.0017 (2.1e-4) for their own rounding alone and in two parts, 0.0023 (2.8e-4) in one. Over a paged cache, bound by
+// memory, two parts take 373 us for 369 (64 sequences of 8000 tokens) and 33.2 for 32.9 (one of 32768), and are taken;
+// over packed prompts 750 for 550 (8192 rows, 32 and 8 heads of 128) and 70 for 58 (16 and 2 heads of 64 in 8
+// sequences), and one is.
 template <class T>
 struct Weights {
     Piece w[2];
@@ -153,6 +158,18 @@ struct Weights {
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[t][i] = word_of<T>(s[8 * t + 2 * i], s[8 * t + 2 * i + 1]);
+    }
+    // s less what was taken of it.
+    __device__ __forceinline__ floatx16 rest(const floatx16& s) const {
+        floatx16 r;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            Raw8<T> x;
+            __builtin_memcpy(&x, &w[t], 16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[8 * t + e] = s[8 * t + e] - x.at(e);
+        }
+        return r;
     }
 };
 template <>

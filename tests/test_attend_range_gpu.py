@@ -311,3 +311,37 @@ def check_small(q, k, v, dout, lengths, heads, kv, scale, what):
         want, bound = exact_backward(q[r], k[r], v[r], dout[r], heads, kv, False, scale, score_sums=True)
         for a, w, b, name in zip(got, want, bound, ("dq", "dk", "dv")):
             check(a[r], w, b, f"{what}: {name}")
+
+
+# ------------------------------------------------------- the paged form's weights
+
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("lengths,heads,kv,dim,page", [
+    ([5000], 8, 2, 128, 16), ([255, 1, 33, 700], 4, 2, 64, 16), ([900, 2], 10, 5, 80, 49), ([40] * 9, 4, 4, 33, 8)])
+def test_paged_weights_are_not_rounded_to_the_caches_type(dt, lengths, heads, kv, dim, page):
+    """Outputs are off by their own rounding and fp32's sums; weights, in two parts of the type, by its square."""
+    from tests.test_attend_gpu import pool
+    say("paged weights", dt, lengths, heads, kv, dim, page)
+    kp, vp, table = pool(dt, lengths, kv, dim, page)
+    q = (1.5 * rand(len(lengths), heads * dim, seed=3)).to(dt)
+    out = torch.empty_like(q)
+    scale = dim ** -0.5
+    tte.tt_emb_attend_paged(q, kp, vp, table, torch.tensor(lengths, device=DEV), out)
+    g = heads // kv
+    want, bound = (torch.empty(len(lengths), heads, dim, dtype=F64, device=DEV) for _ in range(2))
+    kd = product_slack(dim)
+    for i, n in enumerate(lengths):
+        j = torch.arange(n, device=DEV)
+        slot = table[i].long()[j // page] * page + j % page
+        k, v = (x.view(-1, kv, dim)[slot].double().transpose(0, 1).repeat_interleave(g, 0) for x in (kp, vp))
+        x = q[i].double().view(heads, 1, dim)
+        s = scale * x @ k.mT
+        p = torch.softmax(s, -1)
+        e = kd * scale * (x.abs() @ k.abs().mT) + 4 * U32 * (1 + s.abs())
+        kn = product_slack(2 * n)
+        # (f16: weights are at 2^8 of the largest, half a step below its normal numbers is 2^-25)
+        low = 2.0 ** -33 * p.amax(-1, keepdim=True) if dt == F16 else 2.0 ** -126
+        o = p @ v
+        b = rounded(dt, o) + (p * (e + 2 * U[dt] ** 2 + kn) + low) @ v.abs() + o.abs() * ((p * e).sum(-1, keepdim=True) + kn)
+        want[i], bound[i] = o[:, 0], b[:, 0]
+    check(out, want.flatten(1), bound.flatten(1), "paged weights")
