@@ -469,8 +469,10 @@ tt_status tt_emb_rotate_forward(int32_t dtype, int32_t wdtype, const void* q, in
  * values as they are, go into the paged cache: row r's to slot slots[r] of
  * k_pages and v_pages, [num_slots][kv_heads * dim] (slot = page * page size +
  * place in the page). A row whose slot is outside [0, num_slots) is kept
- * nowhere (its q_out is written all the same); slots named twice hold either
- * row's, in no order. */
+ * nowhere (its q_out is written all the same). Of a slot that several rows name
+ * each element is one of theirs, in no order: parts of one row beside parts of
+ * another, not the same on every run. Rows that are to go nowhere (padding)
+ * name -1. */
 tt_status tt_emb_rotate_append(int32_t dtype, int32_t wdtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
                                const void* v, int64_t ldv, const void* q_weight, const void* k_weight,
                                const int64_t* positions, const double* freq, int64_t rot, int32_t pairs,

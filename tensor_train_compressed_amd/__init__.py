@@ -824,7 +824,7 @@ def tt_emb_rotate_append(q, k, v, q_weight, k_weight, positions, freq, slots, q_
                          pairs: str = "halves", eps: float = 1e-6, stream=None):
     """tt_emb_rotate_forward whose keys, with the values v, go into the paged cache
     [pages, page_size, kv_heads, dim], row r's to place slots[r] (int64) of all pages' in a row; rows whose
-    slot lies outside the cache are kept nowhere."""
+    slot lies outside the cache are kept nowhere. No slot is to be named twice (it would hold parts of either row)."""
     args, (rows, heads, kv, dim) = _rotate_sizes(q, k, q_weight, k_weight, positions, freq, pairs)
     pkp, pvp, shape = _pages(k_pages, v_pages, q.dtype, kv * dim)
     _launch("tt_emb_rotate_append", q, stream, *args[:6], *_matrix(v, q.dtype, "v", rows, kv * dim), *args[6:],

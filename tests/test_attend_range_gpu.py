@@ -345,3 +345,29 @@ def test_paged_weights_are_not_rounded_to_the_caches_type(dt, lengths, heads, kv
         b = rounded(dt, o) + (p * (e + 2 * U[dt] ** 2 + kn) + low) @ v.abs() + o.abs() * ((p * e).sum(-1, keepdim=True) + kn)
         want[i], bound[i] = o[:, 0], b[:, 0]
     check(out, want.flatten(1), bound.flatten(1), "paged weights")
+
+
+# ----------------------------------------------------------- slots named twice
+
+@TYPES
+def test_append_to_slots_named_twice(dt):
+    """Each element of such a slot is one of the rows' that name it; the other slots and the queries are as ever."""
+    rows, heads, kv, dim = 60, 8, 4, 128
+    q, k, v = (rand(rows, n * dim, seed=s, dt=dt) for n, s in ((heads, 1), (kv, 2), (kv, 3)))
+    w, pos = torch.ones(dim, device=DEV), torch.arange(rows, device=DEV)
+    freq = torch.tensor([0.1 * i for i in range(dim // 2)], dtype=F64, device=DEV)
+    slots = torch.arange(rows, device=DEV) + 3
+    slots[10], slots[40], slots[41] = slots[11].item(), slots[50].item(), slots[50].item()
+    caches = [torch.full((80, kv * dim), 7.0, dtype=dt, device=DEV) for _ in range(2)]
+    q_out = torch.empty_like(q)
+    tte.tt_emb_rotate_append(q, k, v, w, w, pos, freq, slots, q_out, *(c.view(10, 8, kv, dim) for c in caches))
+    want_q, want_k = torch.empty_like(q), torch.empty_like(k)
+    tte.tt_emb_rotate_forward(q, k, w, w, pos, freq, want_q, want_k)
+    assert torch.equal(q_out, want_q)
+    for c, rows_of in zip(caches, (want_k, v)):
+        for slot in range(80):
+            named = (slots == slot).nonzero().flatten()
+            if not named.numel():
+                assert bool((c[slot] == 7.0).all())
+            else:
+                assert bool((c[slot] == rows_of[named]).any(0).all()), slot
