@@ -99,18 +99,6 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
         if (i + 1 < i1) issue(i + 1, tq, td);
         const int q0 = (begin + i % per) * BM;
         const bool far = __builtin_amdgcn_readfirstlane(reinterpret_cast<const int*>(st)[3 * BM]) != 0;
-        auto scores = [&](int b, floatx16& s, floatx16& dp) TT_INLINE {
-            s = dp = floatx16{};
-#pragma unroll
-            for (int x = 0; x < L::STEPS; ++x) {
-                if constexpr (GROUPS == 2) {
-                    fk[x] = L::row_piece(sk, mine * kQueries, x);
-                    fv[x] = L::row_piece(sv, mine * kQueries, x);
-                }
-                s = mma_rows<T>(L::row_piece(sq, 32 * b, x), fk[x], s);
-                dp = mma_rows<T>(L::row_piece(sd, 32 * b, x), fv[x], dp);
-            }
-        };
         auto weights = [&](int b, floatx16& s, floatx16& dp) TT_INLINE {
             if (far) {
 #pragma unroll
@@ -133,13 +121,6 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
                     s[r] = exp2_hw(fmaf(s[r], c, -lg[e]));
                     dp[r] = s[r] * (dp[r] - dg[e]);
                 }
-            }
-        };
-        auto sums = [&](int b, const Weights<T>& ws, const Weights<T>& wd) TT_INLINE {
-#pragma unroll
-            for (int j = 0; j < DP / 32; ++j) {
-                dv[j] = mma_columns<T, DP>(sd, 32 * b, j, ws, dv[j]);
-                dk[j] = mma_columns<T, DP>(sq, 32 * b, j, wd, dk[j]);
             }
         };
         if constexpr (sizeof(T) == 2) {
@@ -208,8 +189,12 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
             for (int n = 0; n < BLOCKS / GROUPS; ++n) {
                 const int b = GROUPS * n + group, first_q = q0 + 32 * b;
                 if (first_q >= sp.len || (a.causal && first_q + 31 < k0)) continue;
-                floatx16 s, dp;
-                scores(b, s, dp);
+                floatx16 s = {}, dp = {};
+#pragma unroll
+                for (int x = 0; x < L::STEPS; ++x) {
+                    s = mma_rows<T>(L::row_piece(sq, 32 * b, x), fk[x], s);
+                    dp = mma_rows<T>(L::row_piece(sd, 32 * b, x), fv[x], dp);
+                }
                 weights(b, s, dp);
                 if (first_q + 32 > sp.len || (a.causal && first_q < k0 + 31)) {
 #pragma unroll
@@ -221,7 +206,11 @@ __global__ __launch_bounds__(GROUPS * KEYS * 64, (waves_of<T, DP, DMA, DKV>())) 
                 Weights<T> ws, wd;
                 ws.set(s);
                 wd.set(dp);
-                sums(b, ws, wd);
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    dv[j] = mma_columns<T, DP>(sd, 32 * b, j, ws, dv[j]);
+                    dk[j] = mma_columns<T, DP>(sq, 32 * b, j, wd, dk[j]);
+                }
             }
         }
         if (i + 1 < i1) store(tq, td, ts);
