@@ -527,7 +527,10 @@ tt_status tt_emb_attend_backward(int32_t dtype, const void* q, int64_t ldq, cons
  * already). A length past most_pages * page_size counts as that, one below zero
  * as zero; a token whose page is outside [0, pages) is not seen; a sequence
  * that sees nothing gives 0. With 16-bit types weights meet v in two parts of
- * dtype, so that their rounding does not show beside the output's.
+ * dtype, so that their rounding does not show beside the output's; an infinity
+ * or NaN in a value that is seen makes that element of the heads that read it
+ * infinite or NaN, one in a key all of theirs (a score of -inf: not seen), and no
+ * other head's or sequence's. Places that are not seen may hold anything.
  *   table  int32, most_pages entries a sequence, ldt apart
  * The workspace serves any lengths, and fewer sequences.
  * Limits: 0 < scale < 2e38; dim <= 128, heads / kv_heads <= 256,

@@ -371,3 +371,41 @@ def test_append_to_slots_named_twice(dt):
                 assert bool((c[slot] == 7.0).all())
             else:
                 assert bool((c[slot] == rows_of[named]).any(0).all()), slot
+
+
+@TYPES
+@pytest.mark.parametrize("length", [70, 3000])
+def test_paged_infinities_stay_in_their_element(dt, length):
+    """An infinity in a seen value reaches its element of the heads that read it, one in a token that is not seen nothing; a
+    key whose scores are -inf is not seen."""
+    heads, kv, dim, page = 4, 2, 64, 16
+    pages = (length + page - 1) // page
+    kp, vp = (rand(pages, page, kv, dim, seed=s, dt=dt) for s in (1, 2))
+    q = rand(1, heads * dim, seed=3, dt=dt)
+    table, lens = torch.arange(pages, device=DEV).to(I32)[None], torch.tensor([length - 3], device=DEV)
+    good = torch.empty_like(q)
+    tte.tt_emb_attend_paged(q, kp, vp, table, lens, good)
+    bad = torch.empty_like(q)
+    vp.view(-1, kv, dim)[length - 3:length, :] = float("inf")      # behind the sequence's last
+    kp.view(-1, kv, dim)[length - 3:length, :] = float("nan")
+    tte.tt_emb_attend_paged(q, kp, vp, table, lens, bad)
+    assert torch.equal(good, bad)
+    for value in (float("inf"), -float("inf"), float("nan")):
+        vp.view(-1, kv, dim)[5, 1, 7] = value
+        tte.tt_emb_attend_paged(q, kp, vp, table, lens, bad)
+        hit = torch.zeros(heads, dim, dtype=torch.bool, device=DEV)
+        hit[2:, 7] = True
+        assert torch.equal(~torch.isfinite(bad.view(heads, dim)), hit)
+        assert torch.equal(bad.view(heads, dim)[~hit], good.view(heads, dim)[~hit])
+    # keys whose scores are -inf: as if they were not there
+    vp.view(-1, kv, dim)[5, 1, 7] = 0.0
+    kp.view(-1, kv, dim)[9, :, 3] = -float("inf")
+    x = q.clone().view(heads, dim)
+    x[:, 3] = x[:, 3].abs() + 0.5
+    x = x.view(1, -1)
+    tte.tt_emb_attend_paged(x, kp, vp, table, lens, bad)
+    keep = torch.tensor([j for j in range(length - 3) if j != 9], device=DEV)
+    k2, v2 = (torch.zeros(pages * page, kv, dim, dtype=dt, device=DEV) for _ in range(2))
+    k2[:len(keep)], v2[:len(keep)] = kp.view(-1, kv, dim)[keep], vp.view(-1, kv, dim)[keep]
+    want, bound = ref.paged(x, k2.view(pages, page, kv, dim), v2.view(pages, page, kv, dim), table, lens - 1, dim ** -0.5)
+    check(bad, want, bound, "beside a key of -inf")
