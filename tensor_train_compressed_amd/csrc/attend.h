@@ -40,12 +40,16 @@ constexpr int AHEAD = 4;
 
 constexpr int kQueries = 32;   // a wave's
 
-// Waves of a workgroup: four, or one where sequences are short (and rows in whole pieces), whose
+// Waves of a workgroup: four, or one where sequences are short on average (and rows in whole pieces), whose
 // tiles the other three would have no part in. 16384 rows in sequences of equal length, us of the
 // forward and of the backward, one wave and four:
-//   4 heads of 32 fp32            20 rows 17 44, 50 120;  64 rows 15 44, 20 59;  128 rows 21 57, 28 86;  192 rows 24 66, 26 80
-//   16 and 4 heads of 64 bf16     20 rows 49 99, 129 214; 64 rows 46 97, 55 112; 128 rows 46 104, 85 179; 192 rows 48 116, 56 130
-//   32 and 8 heads of 128 bf16    20 rows 206 438, 333 905; 64 rows 174 388, 181 447; 128 rows 184 425, 174 505; 192 rows 192 467, 186 448
+//   rows a sequence      20                 64                96                128               192
+//   4 heads of 32 fp32   17 45, 49 118      15 44, 20 59      25 68, 21 66      21 57, 29 85      25 68, 27 88
+//   16 / 4 of 64 bf16    48 99, 128 211     45 96, 57 109     57 130, 53 112    46 106, 85 178    50 118, 57 129
+//   32 / 8 of 128 bf16   206 437, 333 873   175 387, 181 440  179 452, 185 434  184 422, 174 494  193 460, 185 442
+// The average also counts sequences without rows, and does not see one long sequence among many short ones; there
+// four would take less (32 and 8 heads of 128 bf16): 7000 rows among 100 sequences of 10 803 2022, 546 1556; 8192 rows
+// beside 255 empty sequences 944 2486, 590 1899.
 constexpr int kWaves = 4;
 constexpr int64_t kShort = 128;   // rows a sequence, on average, up to which
 
@@ -57,7 +61,8 @@ constexpr int tile_rows() {
 
 // Waves a SIMD is to hold: two where their registers allow it without spilling (loads from where
 // registers were spilled to wait for all that is under way to LDS, which took a kernel from 560 to
-// 1230 us).
+// 1230 us). dk and dv of 16-bit heads past 64 have two by their groups of waves; there rows that go through registers
+// spill up to 43 of them (2948 unaligned rows, 8 heads of 127 bf16, dq, dk and dv: 533 us).
 enum Pass { FWD, DQ, DKV };
 template <class T, int DP, bool DMA, Pass PASS>
 constexpr int waves_of() {

@@ -15,14 +15,15 @@
 // What bounds it, and what it measures: one prompt of 8192 rows, 32 and 8 heads of 128 bf16, causal,
 // 555 us, 990 TFLOP/s of what is not masked. Without the loads of tiles 480, without the softmax
 // 480, without both 405 (1360 TFLOP/s), all at 1.9 GHz of 2.4: matrix and vector instructions of
-// a SIMD's two waves overlap in part, and power holds the clock. LDS is busy a quarter of the time, with no bank
-// conflict. Measured the same or slower: a block of keys ahead, its scores formed beside the weights
+// a SIMD's two waves overlap in part, and power holds the clock. The matrix cores are busy 55% of the time, LDS 27%,
+// with no bank conflict. Measured the same or slower: a block of keys ahead, its scores formed beside the weights
 // of the one before, instruction by instruction (560 to 600); two blocks of queries a wave (its accumulators
 // spill); priorities of waves (570).
 //
 // The backward forms scores twice, once by queries (dq) and once by keys (dk and dv): seven
 // products instead of five, but each result is summed by one wave in a fixed order, without
-// atomics. Of the same prompt dq takes 710 us (1160 TFLOP/s), dk and dv 1215 (905).
+// atomics. Of the same prompt dq takes 740 us (1110 TFLOP/s; matrix cores busy 65%, LDS 33%), dk and dv 1135
+// (970; 50%, 44%).
 //
 // Workgroups: heads that share keys are launched together and, where 8 divides the key
 // heads, on one XCD, whose L2 then holds their keys; of a sequence the tiles with the most

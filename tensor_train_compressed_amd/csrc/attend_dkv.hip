@@ -10,7 +10,7 @@ namespace {
 // KEYS: waves of a tile of keys. GROUPS = 2: two waves a SIMD, where the registers for keys, values and both sums are too
 // many for two (heads of more than 64): the second four waves have the first's keys and take
 // the other half of each tile of queries, keys and values are read from LDS, and the halves' sums
-// meet at the end. One prompt of 8192 rows, 32 and 8 heads of 128 bf16: 1215 us; one wave a SIMD with keys and
+// meet at the end. One prompt of 8192 rows, 32 and 8 heads of 128 bf16: 1135 us; one wave a SIMD with keys and
 // values in registers 1500, and 1300 to 1400 with one block's weights formed beside the other's
 // products. Without the loads of tiles 1000 to 1075.
 //

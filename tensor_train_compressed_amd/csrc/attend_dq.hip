@@ -123,7 +123,8 @@ __global__ __launch_bounds__(WAVES * 64, (waves_of<T, DP, DMA, DQ>())) void k_at
                     auto fetch = [&](auto slot) TT_INLINE {
                         constexpr int u = slot, t = u - N;
                         if constexpr (u < N) f[u % AHEAD] = L::row_piece(u % 2 ? sv : sk, 32 * b, u / 2);
-                        else if constexpr (SWEEP == GRADIENT && t < 2 * J) f[u % AHEAD] = L::column_piece(sk, 32 * b + 16 * (t / J), t % J);
+                        else if constexpr (SWEEP == GRADIENT && t < 2 * J)
+                            f[u % AHEAD] = L::column_piece(sk, 32 * b + 16 * (t / J), t % J);
                     };
                     each<AHEAD>(fetch);
                     each<N>([&](auto slot) TT_INLINE {

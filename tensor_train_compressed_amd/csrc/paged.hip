@@ -325,7 +325,9 @@ __global__ __launch_bounds__(256) void k_attend_paged_join(const PagedArgs a) {
 
 // Tokens of a sequence at most: counts past its end stay within 32 bits.
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
-// Workgroups that a call is split to reach.
+// Workgroups that a call is split to reach, by the number of its sequences alone, whose lengths the host does not
+// know: a long one among very many short ones is split too little (256 sequences, one of 131072 tokens and
+// the others of 500, 32 and 8 heads of 128 bf16: 3050 us; without it 107, it alone 121).
 constexpr int64_t kGroups = 2048;
 
 inline int64_t padded_dim(int64_t dim) { return (dim + 31) / 32 * 32; }
