@@ -456,7 +456,9 @@ typedef enum { TT_PAIRS_HALVES = 0, TT_PAIRS_NEIGHBOURS = 1 } tt_pairs;
  *   (u_a cos - u_b sin, u_a sin + u_b cos); elements from rot on stay u.
  *   wdtype  type of q_weight, k_weight [dim] and their gradients: dtype or TT_F32
  *   positions  int64[rows];  freq  double[rot / 2], radians a position
- * A head whose squares' sum overflows fp32 gives 0 (its infinite elements NaN).
+ * A head whose squares' sum overflows fp32 gives 0 (its infinite elements NaN); with
+ * eps 0 one whose squares' sum underflows (zeros, elements below 1e-19) gives
+ * infinities or NaN, as do its gradients.
  * Limits: dim <= 256, heads, kv_heads <= 4096, rows <= 2^24. */
 size_t tt_emb_rotate_workspace_bytes(int32_t dtype, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim);
 tt_status tt_emb_rotate_forward(int32_t dtype, int32_t wdtype, const void* q, int64_t ldq, const void* k, int64_t ldk,

@@ -409,3 +409,37 @@ def test_paged_infinities_stay_in_their_element(dt, length):
     k2[:len(keep)], v2[:len(keep)] = kp.view(-1, kv, dim)[keep], vp.view(-1, kv, dim)[keep]
     want, bound = ref.paged(x, k2.view(pages, page, kv, dim), v2.view(pages, page, kv, dim), table, lens - 1, dim ** -0.5)
     check(bad, want, bound, "beside a key of -inf")
+
+
+# ------------------------------------------------------ norms at the range's ends
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_rotate_heads_past_the_range(dt):
+    """A head whose squares overflow gives 0, and its gradients; one whose squares underflow gives u = x / sqrt(eps), without
+    eps nothing finite. No other head of the row changes."""
+    rows, heads, dim = 4, 3, 32
+    q, k = rand(rows, heads * dim, seed=1, dt=dt), rand(rows, heads * dim, seed=2, dt=dt)
+    w, pos = torch.ones(dim, device=DEV), torch.zeros(rows, dtype=I64, device=DEV)
+    freq = torch.ones(0, dtype=F64, device=DEV)
+    dy = rand(rows, heads * dim, seed=3, dt=dt)
+
+    def both(x, eps):
+        y, ko, dx, dk = (torch.empty_like(q) for _ in range(4))
+        dw = [torch.empty_like(w) for _ in range(2)]
+        tte.tt_emb_rotate_forward(x, k, w, w, pos, freq, y, ko, eps=eps)
+        tte.tt_emb_rotate_backward(x, k, w, w, pos, freq, dy, dy, dx, dk, *dw, eps=eps)
+        return y.view(rows, heads, dim), dx.view(rows, heads, dim)
+    x = q.clone()
+    x[1, :dim] = (q[1, :dim].float() * 1e25).to(dt)
+    x[2, dim:2 * dim] = (q[2, dim:2 * dim].float() * 1e-25).to(dt)
+    others = torch.ones(rows, heads, dtype=torch.bool, device=DEV)
+    others[1, 0] = others[2, 1] = False
+    for eps in (1e-6, 0.0):
+        (y0, d0), (y, d) = both(q, eps), both(x, eps)
+        assert torch.equal(y[others], y0[others]) and torch.equal(d[others], d0[others])
+        assert bool((y[1, 0] == 0).all() and (d[1, 0] == 0).all())
+        if eps:
+            want = x.view(rows, heads, dim)[2, 1].double() / eps ** 0.5
+            check(y[2, 1], want, rounded(dt, want) + 8 * U32 * want.abs(), "below eps")
+        else:
+            assert not bool(torch.isfinite(y[2, 1]).any())
