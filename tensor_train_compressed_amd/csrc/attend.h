@@ -74,6 +74,7 @@ constexpr int waves_of() {
 // A sum's f16 factors (the backward's ds), times a power of two 2^up that keeps the largest of a column that was
 // seen between 2^9 and 2^15: none is past f16's range, and those down to 2^-23 of the largest keep their digits.
 // The power falls where a factor outgrows it, and sums are multiplied by what it fell. Other types hold any factor.
+// 2048 rows, heads of 64, dout of size 1e-4: dq's 2-norm error 1.6e-2 without it, 2.4e-3 with, as for rounding dq alone.
 // Its cost, dq, dk and dv together: 8192 rows, 32 and 8 heads of 128, 1900 -> 2000 us; 16 and 2 heads of 64 in 8
 // sequences 185 -> 200.
 template <class T>
