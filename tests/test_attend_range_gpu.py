@@ -443,3 +443,70 @@ def test_rotate_heads_past_the_range(dt):
             check(y[2, 1], want, rounded(dt, want) + 8 * U32 * want.abs(), "below eps")
         else:
             assert not bool(torch.isfinite(y[2, 1]).any())
+
+
+# ------------------------------------------------------------- graphs, streams
+
+class Step:
+    """One training step of attention on buffers of its own."""
+
+    def __init__(self, dt, seed):
+        self.dt, self.heads, self.kv, self.dim, self.rows = dt, 8, 2, 64, 400
+        self.q, self.k, self.v, self.d = (rand(self.rows, n * self.dim, seed=seed + i, dt=dt)
+                                          for i, n in enumerate((self.heads, self.kv, self.kv, self.heads)))
+        self.off = offsets_of([150, 0, 230, 20])
+        size = tte.tt_emb_attend_workspace_bytes(dt, self.rows, self.heads, self.kv, self.dim)
+        self.ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        self.res = self.buffers()
+
+    def buffers(self):
+        return [torch.zeros_like(t) for t in (self.q, self.q, self.k, self.v)] + [torch.zeros(self.heads, self.rows, device=DEV)]
+
+    def run(self, res, stream=None):
+        out, dq, dk, dv, lse = res
+        how = dict(heads=self.heads, kv_heads=self.kv, scale=0.125, stream=stream)
+        tte.tt_emb_attend_forward(self.q, self.k, self.v, self.off, out, lse, **how)
+        tte.tt_emb_attend_backward(self.q, self.k, self.v, self.off, out, lse, self.d, dq, dk, dv, workspace=self.ws, **how)
+
+
+@TYPES
+def test_captured_backward_from_near_scores_to_far_and_back(dt):
+    """Which rows form their sum again is found on the device: a captured step does as the eager one for every input."""
+    s = Step(dt, 1)
+    s.run(s.res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.run(s.res)
+    for i, (far, grad) in enumerate(((1.0, 1.0), (3000.0, 2.0 ** -8), (1.0, 2.0 ** -12), (300.0, 1.0))):
+        q = rand(*s.q.shape, seed=20 + i)
+        q[::2] *= far
+        s.q.copy_(q.to(dt))
+        s.d.copy_((rand(*s.d.shape, seed=30 + i) * grad).to(dt))
+        graph.replay()
+        got = [t.clone() for t in s.res]
+        torch.cuda.synchronize()
+        assert (float(got[4].abs().max()) > TRUSTED[dt]) == (far > 1)
+        eager = s.buffers()
+        s.run(eager)
+        for a, b in zip(got, eager):
+            assert bool(torch.isfinite(a).all()) and torch.equal(a, b), i
+
+
+@TYPES
+def test_two_steps_at_once(dt):
+    """Two steps on two streams, one of far scores, each with a workspace of its own."""
+    steps = [Step(dt, 1), Step(dt, 11)]
+    steps[1].q.mul_(300.0)
+    streams = [torch.cuda.Stream() for _ in steps]
+    for s in steps:
+        s.run(s.res)
+    got = [s.buffers() for s in steps]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, st, g in zip(steps, streams, got):
+            s.run(g, stream=st)
+    torch.cuda.synchronize()
+    for s, g in zip(steps, got):
+        for a, b in zip(s.res, g):
+            assert torch.equal(a, b)
